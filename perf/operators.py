@@ -203,6 +203,10 @@ def prepare(case, seed):
             freq = freq * keep + freq / 8 * (1 - keep)
             s["factor"] = 0.1 * math.log(8) + 1
         s["freq"] = freq.float().cuda()
+        if own:
+            import sliding_window_gqa_chunk_b200 as swa
+            s["dims"] = swa.Dims(B, Hq, H, d, 1, 1.0, "bf16")
+            s["rope"] = swa.Rope(s["freq"], case["interleaved"], s["factor"])
         return s
     k8, ks = _ring(gen, case)
     v8, vs = _ring(gen, case)
@@ -213,10 +217,19 @@ def prepare(case, seed):
     if case["op"] != "append":
         s["q"] = torch.randn((*shape, Hq, d), generator=gen, device="cuda").to(torch.bfloat16)
         s["out"] = torch.randn((*shape, Hq, d), generator=gen, device="cuda").to(torch.bfloat16)
-    if own and case["op"] in ("prefill", "decode"):
-        import sliding_window_gqa_chunk_b200 as swa
-        dims = swa.Dims(B, Hq, H, d, case["window"], s["scale"], "bf16")
-        s["ws"] = swa.prefill_workspace_q8(dims, T) if case["op"] == "prefill" else swa.decode_workspace_q8(dims)
+    return _handles(s) if own else s
+
+
+def _handles(s):
+    """What a user's program keeps beside its tensors: the dims, the cache's handle and a workspace."""
+    import sliding_window_gqa_chunk_b200 as swa
+    c = s["case"]
+    s["dims"] = swa.Dims(c["batch"], c["q_heads"], c["kv_heads"], c["dim"], c["window"], s["scale"], "bf16")
+    s["cache"] = swa.CacheQ8(s["k8"], s["v8"], s["ks"], s["vs"], s["kt"], s["vt"])
+    if c["op"] == "prefill":
+        s["ws"] = swa.prefill_workspace_q8(s["dims"], c["tokens"])
+    elif c["op"] == "decode":
+        s["ws"] = swa.decode_workspace_q8(s["dims"])
     return s
 
 
@@ -354,19 +367,16 @@ def run(state):
     if not own:
         return {"rope": _plain_rope, "append": _plain_append, "decode": _plain_decode, "prefill": _plain_prefill}[c["op"]](s)
     import sliding_window_gqa_chunk_b200 as swa
-    dims = swa.Dims(c["batch"], c["q_heads"], c["kv_heads"], c["dim"], c.get("window", 1), s.get("scale", 1.0), "bf16")
     if c["op"] == "rope":
-        rotary = swa.Rope(s["freq"], c["interleaved"], s["factor"])
-        swa.rope(dims, rotary, s["q_out"], s["k_out"], s["q"], s["k"], s["start"], s["count"], transpose=c["transpose"])
+        swa.rope(s["dims"], s["rope"], s["q_out"], s["k_out"], s["q"], s["k"], s["start"], s["count"], transpose=c["transpose"])
         return s["q_out"], s["k_out"]
-    cache = swa.CacheQ8(s["k8"], s["v8"], s["ks"], s["vs"], s["kt"], s["vt"])
     if c["op"] == "append":
-        swa.cache_append_q8(dims, cache, s["k"], s["v"], s["start"], s["count"])
+        swa.cache_append_q8(s["dims"], s["cache"], s["k"], s["v"], s["start"], s["count"])
         return _cache_out(s)
     if c["op"] == "prefill":
-        swa.prefill_chunk_q8(dims, s["out"], s["q"], s["k"], s["v"], cache, s["start"], s["count"], s["ws"])
+        swa.prefill_chunk_q8(s["dims"], s["out"], s["q"], s["k"], s["v"], s["cache"], s["start"], s["count"], s["ws"])
         return s["out"]
-    swa.decode_q8(dims, s["out"], s["q"], s["k"], s["v"], cache, s["start"], s["ws"])
+    swa.decode_q8(s["dims"], s["out"], s["q"], s["k"], s["v"], s["cache"], s["start"], s["ws"])
     return [s["out"], *_cache_out(s)]
 
 
