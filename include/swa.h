@@ -213,6 +213,135 @@ SWA_API int swa_decode_static(const swa_dims* dims, void* out, const void* q, co
                       void* stream);
 
 /*
+ * The 8-bit rolling cache.  swa_q8_append, swa_q8_prefill_chunk and
+ * swa_q8_decode do what swa_cache_append, swa_prefill_chunk and swa_decode do,
+ * over a cache that holds keys and values in 8 bits (half the bytes that a
+ * decode step has to read).
+ *
+ * The W slots are divided into blocks of SWA_Q8_BLOCK (slots [64 j, 64 j + 64);
+ * the last block of a ring whose W is not a multiple of 64 is shorter).  The
+ * rows of a block are held as 8-bit numbers with one scale for the keys and one
+ * for the values of each kv head: the smallest power of two (at least 2^-100)
+ * that brings the block's largest magnitude into the format's range (448 for
+ * e4m3, 127 for int8), or 1 for a block of zeros.  A row is held as
+ * round-to-nearest-even(x / scale).
+ * While a block is being filled, its new rows are in the tail, in bf16; they
+ * are rounded once, together, by the call that brings the block's last row, and
+ * until then the block still holds the rows of the ring's previous lap.  So what
+ * the cache holds depends on the tokens alone, not on how they were cut into
+ * calls, and the value that a row stands for (8-bit number times scale) is
+ * exact in bf16: prefill and decode attend to the same numbers.
+ *
+ * Before the first token of a sequence no contents matter (the calls read no
+ * row, scale or tail row that was not written before), but for the prefill
+ * workspace.  A sequence's tokens are taken in in order: start_pos / pos is the
+ * number of tokens that it has taken in so far (any number, for a sequence
+ * begun anew, if start_pos is 0).
+ * Keys and values must be finite; what an infinity or a NaN leaves in its block
+ * is not defined, and harms no other block, head or sequence.
+ */
+#define SWA_Q8_BLOCK 64
+#define SWA_Q8_E4M3 0 /* 8-bit floating point: 4 exponent bits, 3 mantissa bits, no infinities */
+#define SWA_Q8_INT8 1 /* whole numbers -127 .. 127 */
+
+typedef struct swa_q8_cache {
+    void*   k;       /* [B][Hkv][W][d], one byte an element                         */
+    void*   v;
+    float*  k_scale; /* [B][Hkv][ceil(W / 64)] powers of two                         */
+    float*  v_scale;
+    void*   k_tail;  /* [B][Hkv][64][d] bf16: row i is slot 64 j + i of the block j  */
+    void*   v_tail;  /* that the sequence's next token falls into, if i is before it */
+    int32_t format;  /* SWA_Q8_E4M3 or SWA_Q8_INT8                                   */
+} swa_q8_cache;
+
+/*
+ * swa_q8_append - swa_cache_append for the 8-bit cache (same k, v, max_tokens,
+ * start_pos and n_tokens).  Blocks that the chunk fills up are rounded into the
+ * cache; the rows of the block that it leaves unfilled go to the tail.  Issue it
+ * after swa_q8_prefill_chunk of the same chunk.
+ */
+SWA_API int swa_q8_append(const swa_dims* dims, const swa_q8_cache* cache, const void* k, const void* v,
+                  int32_t max_tokens, const int32_t* start_pos, const int32_t* n_tokens,
+                  void* stream);
+
+/*
+ * swa_q8_prefill_workspace_size - bytes of device scratch swa_q8_prefill_chunk
+ * needs: that of swa_prefill_chunk, and room for this layer's ring in bf16
+ * (4 B Hkv W d bytes; one workspace serves all layers of a model in turn).
+ * Depends only on its arguments.  Returns 0 for invalid arguments.
+ */
+SWA_API size_t swa_q8_prefill_workspace_size(const swa_dims* dims, int32_t max_tokens);
+
+/*
+ * swa_q8_prefill_chunk - swa_prefill_chunk over the 8-bit cache (which it does
+ * not change).  The chunk's own keys and values are attended to as they are
+ * given, in bf16.
+ *   workspace   at least swa_q8_prefill_workspace_size(dims, max_tokens) bytes,
+ *               16-byte aligned, ZERO-FILLED before its first use and again
+ *               before it serves other dims.  Calls that may overlap on the GPU
+ *               need separate workspaces.
+ */
+SWA_API int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const void* k,
+                         const void* v, int32_t max_tokens, const swa_q8_cache* cache,
+                         const int32_t* start_pos, const int32_t* n_tokens, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* swa_q8_decode_workspace_size - as swa_decode_workspace_size, for swa_q8_decode. */
+SWA_API size_t swa_q8_decode_workspace_size(const swa_dims* dims);
+
+/*
+ * swa_q8_decode - swa_decode over the 8-bit cache: the new key and value of
+ * position pos[b] are taken in (into the tail, or with the tail into the cache
+ * if they fill a block up), and the query attends over the min(pos[b] + 1, W)
+ * positions (pos[b] - W, pos[b]], the block being filled in bf16.
+ * Other arguments as in swa_decode.
+ */
+SWA_API int swa_q8_decode(const swa_dims* dims, void* out, const void* q, const void* k_new,
+                  const void* v_new, const swa_q8_cache* cache, const int32_t* pos,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions.  The first rotary_dim elements of each head's row are
+ * taken as pairs, pair i being elements (i, i + rotary_dim / 2), or with
+ * `interleaved` elements (2 i, 2 i + 1); the pair (a, b) of the row at position
+ * p becomes factor * (a cos t - b sin t, b cos t + a sin t), t = p * inv_freq[i].
+ * The other elements are passed through.  Scaled forms for long contexts are
+ * other tables (and, for some, a factor).
+ */
+typedef struct swa_rope_spec {
+    const float* inv_freq;    /* device float32[rotary_dim / 2]                     */
+    int32_t      rotary_dim;  /* a multiple of 16, 16 <= rotary_dim <= head_dim     */
+    int32_t      interleaved; /* 0: pairs (i, i + rotary_dim / 2); 1: (2 i, 2 i + 1) */
+    float        factor;      /* multiplier of the rotated elements, finite and > 0 */
+} swa_rope_spec;
+
+/*
+ * swa_rope - turn a chunk's q and k to their positions, before
+ * swa_prefill_chunk / swa_cache_append (with max_tokens = 1, before swa_decode).
+ *
+ *   q_out, k_out  [B][max_tokens][Hq][d] and [B][max_tokens][Hkv][d] bf16; rows
+ *                 t >= n_tokens[b] are not written
+ *   q, k          the same shapes, bf16, with q_stride / k_stride elements from
+ *                 a token's row to the next one's (max_tokens * stride from a
+ *                 sequence to the next): Hq * d / Hkv * d for dense tensors, more
+ *                 for heads inside a packed projection; multiples of 8
+ *   in place      q_out may be q and k_out may be k if they are dense; other
+ *                 overlaps of an output with any input are not allowed
+ *   k, k_out      both may be NULL: q alone is turned
+ *   max_tokens    >= 1, B * max_tokens < 2^31
+ *   start_pos     device int32[B], >= 0: row t is at position start_pos[b] + t
+ *   n_tokens      device int32[B], 0 <= n_tokens[b] <= max_tokens, or NULL: all
+ *   transpose     0, or 1 for the transposed map (angles -t, same factor): the
+ *                 gradient with respect to q and k from that of q_out and k_out
+ * dims->window, scale and out_dtype are not used but must be valid.  The angle is
+ * the product of position and inv_freq in 64 bits, so far positions keep it.
+ */
+SWA_API int swa_rope(const swa_dims* dims, const swa_rope_spec* spec, void* q_out, void* k_out,
+             const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+             int32_t max_tokens, const int32_t* start_pos, const int32_t* n_tokens,
+             int32_t transpose, void* stream);
+
+/*
  * swa_device_status - synchronise `stream`, then read and clear the library's
  * device status word on the current device: SWA_OK, SWA_ERR_TIMEOUT (a
  * bounded wait inside a kernel ran out; that kernel's outputs are invalid) or

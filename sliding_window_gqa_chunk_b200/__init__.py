@@ -23,11 +23,27 @@ Typical use for one layer::
         cache_append(dims, kc, vc, k, v, start_pos, n_tokens)
     ws = decode_workspace(dims)
     decode(dims, out1, q1, k1, v1, kc, vc, pos, ws)  # one token per sequence
+
+The same over a cache held in 8 bits (half the bytes of a decode step), with the
+rotary positions of q and k::
+
+    rot = new_rope(128, base=10000.0)               # table of frequencies
+    cache = new_cache_q8(dims, "e4m3")
+    pws = prefill_workspace_q8(dims, max_tokens=4096)
+    for chunk ...:
+        rope(dims, rot, q, k, q, k, start_pos, n_tokens)          # in place
+        prefill_chunk_q8(dims, out, q, k, v, cache, start_pos, n_tokens, pws)
+        cache_append_q8(dims, cache, k, v, start_pos, n_tokens)
+    ws = decode_workspace_q8(dims)
+    rope(dims, rot, q1, k1, q1, k1, pos)            # [B, 1, heads, d] views of the step's q, k
+    decode_q8(dims, out1, q1, k1, v1, cache, pos, ws)
 """
 from __future__ import annotations
 
 import ctypes
+import contextlib
 import dataclasses
+import math
 import os
 import threading
 from typing import Optional
@@ -38,6 +54,9 @@ __all__ = [
     "Dims", "SwaError", "load_library", "library_path", "cache_append", "prefill_chunk",
     "decode", "decode_static", "decode_workspace_size", "decode_workspace", "decode_launch_info",
     "prefill_workspace_size", "prefill_workspace", "device_status", "new_cache", "abi_version",
+    "CacheQ8", "new_cache_q8", "cache_append_q8", "prefill_workspace_size_q8", "prefill_workspace_q8",
+    "prefill_chunk_q8", "decode_workspace_size_q8", "decode_workspace_q8", "decode_q8", "Q8_BLOCK",
+    "Rope", "new_rope", "rope",
     "SWA_OK", "SWA_ERR_INVALID_ARG", "SWA_ERR_UNSUPPORTED", "SWA_ERR_WORKSPACE_TOO_SMALL",
     "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT", "SWA_ERR_DEVICE_ARG",
 ]
@@ -70,6 +89,17 @@ class _CDims(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("out_dtype", ctypes.c_int32)]
+
+
+class _CCacheQ8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p),
+                ("v_tail", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float)]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -125,6 +155,20 @@ def load_library() -> ctypes.CDLL:
         lib.swa_decode.restype = ctypes.c_int
         lib.swa_decode_static.argtypes = [D, P, P, P, P, P, P, P, P]
         lib.swa_decode_static.restype = ctypes.c_int
+        C = ctypes.POINTER(_CCacheQ8)
+        lib.swa_q8_append.argtypes = [D, C, P, P, I32, P, P, P]
+        lib.swa_q8_append.restype = ctypes.c_int
+        lib.swa_q8_prefill_workspace_size.argtypes = [D, I32]
+        lib.swa_q8_prefill_workspace_size.restype = ctypes.c_size_t
+        lib.swa_q8_prefill_chunk.argtypes = [D, P, P, P, P, I32, C, P, P, P, ctypes.c_size_t, P]
+        lib.swa_q8_prefill_chunk.restype = ctypes.c_int
+        lib.swa_q8_decode_workspace_size.argtypes = [D]
+        lib.swa_q8_decode_workspace_size.restype = ctypes.c_size_t
+        lib.swa_q8_decode.argtypes = [D, P, P, P, P, C, P, P, ctypes.c_size_t, P]
+        lib.swa_q8_decode.restype = ctypes.c_int
+        lib.swa_rope.argtypes = [D, ctypes.POINTER(_CRope), P, P, P, P, ctypes.c_int64, ctypes.c_int64,
+                                 I32, P, P, I32, P]
+        lib.swa_rope.restype = ctypes.c_int
         lib.swa_device_status.argtypes = [P]
         lib.swa_device_status.restype = ctypes.c_int
         lib.swa_last_error.argtypes = []
@@ -248,3 +292,246 @@ def decode_static(dims: Dims, out, q, k_new, v_new, k_cache, v_cache, pos, strea
 def device_status(stream=None) -> None:
     """Synchronise and raise SwaError if a kernel flagged a timeout or a bad device argument."""
     _check(load_library().swa_device_status(_stream(stream)))
+
+
+# ---- the 8-bit rolling cache and the rotary positions ----
+#
+# These calls check their tensors (type, shape, device, density) before anything
+# is launched, and run on the device that the tensors are on.
+
+Q8_BLOCK = 64                                   # slots that share a scale
+_Q8_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_Q8_DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+def _arg(name: str, t: torch.Tensor, shape, dtype: torch.dtype, dev: int) -> int:
+    """Address of a dense tensor of this shape, type and device; ValueError for another."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
+
+
+def _workspace(t: torch.Tensor, dev: int):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}, got one on {t.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _device_of(name: str, t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return t.get_device()
+
+
+def _on(dev: int):
+    """Makes `dev` the current device for a call (nothing where it already is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+def _stream_on(stream, dev: int) -> ctypes.c_void_p:
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
+    return _stream(stream)
+
+
+@dataclasses.dataclass(frozen=True, eq=False)
+class CacheQ8:
+    """One layer's rolling cache in 8 bits (mirrors ``swa_q8_cache``).
+
+    ``k``, ``v`` [B, Hkv, W, d] float8_e4m3fn or int8; ``k_scale``, ``v_scale``
+    [B, Hkv, ceil(W / 64)] float32, powers of two: a row stands for its 8-bit
+    numbers times the scale of its block of 64 slots; ``k_tail``, ``v_tail``
+    [B, Hkv, 64, d] bf16: the rows so far of the block being filled.  The tensors
+    are used where they are; keep the handle and pass it to every call.
+    """
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    k_tail: torch.Tensor
+    v_tail: torch.Tensor
+
+    def __post_init__(self):
+        if self.k.dim() != 4 or self.k.dtype not in _Q8_FORMATS:
+            raise ValueError(f"k: expected [B, Hkv, W, d] float8_e4m3fn or int8, got {self.k.dtype} {tuple(self.k.shape)}")
+        B, H, W, d = self.k.shape
+        dev = _device_of("k", self.k)
+        blocks, tail = (B, H, -(-W // Q8_BLOCK)), (B, H, Q8_BLOCK, d)
+        ptrs = [_arg("k", self.k, self.k.shape, self.k.dtype, dev), _arg("v", self.v, self.k.shape, self.k.dtype, dev),
+                _arg("k_scale", self.k_scale, blocks, torch.float32, dev),
+                _arg("v_scale", self.v_scale, blocks, torch.float32, dev),
+                _arg("k_tail", self.k_tail, tail, torch.bfloat16, dev),
+                _arg("v_tail", self.v_tail, tail, torch.bfloat16, dev)]
+        object.__setattr__(self, "_c", _CCacheQ8(*ptrs, _Q8_FORMATS[self.k.dtype]))
+        object.__setattr__(self, "_dev", dev)
+        object.__setattr__(self, "_shape", (B, H, W, d))
+
+    def _for(self, dims: Dims) -> int:
+        """The device of the cache, once it is known to be one of these dims."""
+        if self._shape != (dims.batch, dims.n_kv_heads, dims.window, dims.head_dim):
+            raise ValueError(f"cache of [B, Hkv, W, d] = {self._shape} for {dims}")
+        return self._dev
+
+
+def new_cache_q8(dims: Dims, format: str = "e4m3", device="cuda") -> CacheQ8:
+    """A zeroed 8-bit cache; ``format`` is "e4m3" or "int8" (finer for values of one
+    size, coarser for the small ones of a block that holds large ones)."""
+    if format not in _Q8_DTYPES:
+        raise ValueError(f"format {format!r}: expected one of {sorted(_Q8_DTYPES)}")
+    B, H, W, d = dims.batch, dims.n_kv_heads, dims.window, dims.head_dim
+
+    def zeros(shape, dtype):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    ring, scales, tail = (B, H, W, d), (B, H, -(-W // Q8_BLOCK)), (B, H, Q8_BLOCK, d)
+    return CacheQ8(*(zeros(ring, torch.int8).view(_Q8_DTYPES[format]) for _ in range(2)),
+                   *(zeros(scales, torch.float32) for _ in range(2)),
+                   *(zeros(tail, torch.bfloat16) for _ in range(2)))
+
+
+def cache_append_q8(dims: Dims, cache: CacheQ8, k, v, start_pos, n_tokens, stream=None) -> None:
+    """swa_q8_append: k/v [B, T, Hkv, d] bf16 into the 8-bit cache, blocks that they fill up
+    rounded, the rest in the tail."""
+    dev = cache._for(dims)
+    B, T = dims.batch, int(k.shape[1])
+    rows = (B, T, dims.n_kv_heads, dims.head_dim)
+    args = (_arg("k", k, rows, torch.bfloat16, dev), _arg("v", v, rows, torch.bfloat16, dev), T,
+            _arg("start_pos", start_pos, (B,), torch.int32, dev), _arg("n_tokens", n_tokens, (B,), torch.int32, dev))
+    with _on(dev):
+        _check(load_library().swa_q8_append(ctypes.byref(dims.c()), ctypes.byref(cache._c), *args,
+                                            _stream_on(stream, dev)))
+
+
+def prefill_workspace_size_q8(dims: Dims, max_tokens: int) -> int:
+    return int(load_library().swa_q8_prefill_workspace_size(ctypes.byref(dims.c()), int(max_tokens)))
+
+
+def prefill_workspace_q8(dims: Dims, max_tokens: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for prefill_chunk_q8 with these dims (one serves all layers in turn)."""
+    return torch.zeros(prefill_workspace_size_q8(dims, max_tokens), dtype=torch.uint8, device=device)
+
+
+def prefill_chunk_q8(dims: Dims, out, q, k, v, cache: CacheQ8, start_pos, n_tokens, workspace,
+                     stream=None) -> None:
+    """swa_q8_prefill_chunk: out [B, T, Hq, d] = attention of chunk q over (8-bit cache + chunk k/v)."""
+    dev = cache._for(dims)
+    B, T = dims.batch, int(q.shape[1])
+    heads, rows = (B, T, dims.n_q_heads, dims.head_dim), (B, T, dims.n_kv_heads, dims.head_dim)
+    args = (_arg("out", out, heads, dims.torch_out_dtype, dev), _arg("q", q, heads, torch.bfloat16, dev),
+            _arg("k", k, rows, torch.bfloat16, dev), _arg("v", v, rows, torch.bfloat16, dev), T,
+            ctypes.byref(cache._c),
+            _arg("start_pos", start_pos, (B,), torch.int32, dev), _arg("n_tokens", n_tokens, (B,), torch.int32, dev),
+            *_workspace(workspace, dev))
+    with _on(dev):
+        _check(load_library().swa_q8_prefill_chunk(ctypes.byref(dims.c()), *args, _stream_on(stream, dev)))
+
+
+def decode_workspace_size_q8(dims: Dims) -> int:
+    return int(load_library().swa_q8_decode_workspace_size(ctypes.byref(dims.c())))
+
+
+def decode_workspace_q8(dims: Dims, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of decode_workspace_size_q8(dims) bytes."""
+    return torch.zeros(decode_workspace_size_q8(dims), dtype=torch.uint8, device=device)
+
+
+def decode_q8(dims: Dims, out, q, k_new, v_new, cache: CacheQ8, pos, workspace, stream=None) -> None:
+    """swa_q8_decode: take (k_new, v_new) in at position pos, then out [B, Hq, d] = attention."""
+    dev = cache._for(dims)
+    B, d = dims.batch, dims.head_dim
+    heads, rows = (B, dims.n_q_heads, d), (B, dims.n_kv_heads, d)
+    args = (_arg("out", out, heads, dims.torch_out_dtype, dev), _arg("q", q, heads, torch.bfloat16, dev),
+            _arg("k_new", k_new, rows, torch.bfloat16, dev), _arg("v_new", v_new, rows, torch.bfloat16, dev),
+            ctypes.byref(cache._c), _arg("pos", pos, (B,), torch.int32, dev), *_workspace(workspace, dev))
+    with _on(dev):
+        _check(load_library().swa_q8_decode(ctypes.byref(dims.c()), *args, _stream_on(stream, dev)))
+
+
+@dataclasses.dataclass(frozen=True, eq=False)
+class Rope:
+    """Rotary positions: ``inv_freq`` float32 [r / 2] on the GPU turns the first r elements of each
+    head, as pairs (i, i + r / 2) or, ``interleaved``, (2 i, 2 i + 1); turned elements are
+    multiplied by ``factor``."""
+
+    inv_freq: torch.Tensor
+    interleaved: bool = False
+    factor: float = 1.0
+
+    def __post_init__(self):
+        dev = _device_of("inv_freq", self.inv_freq)
+        n = self.inv_freq.numel()
+        ptr = _arg("inv_freq", self.inv_freq, (n,), torch.float32, dev)
+        object.__setattr__(self, "_c", _CRope(ptr, 2 * n, int(self.interleaved), float(self.factor)))
+        object.__setattr__(self, "_dev", dev)
+
+
+def new_rope(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+             scale: float = 1.0, original_length: int = 4096, device="cuda") -> Rope:
+    """The table base ** (-2 i / rotary_dim), for contexts `scale` times the length a model was
+    trained at (``original_length``) in one of the usual forms:
+
+    * "none";
+    * "linear": all positions divided by scale;
+    * "base": base raised so that the slowest pair turns scale times slower and the fastest as before;
+    * "yarn": pairs that turn more than 32 times over original_length are kept, those that turn less
+      than once are slowed by scale, linearly in the number of turns between, and turned elements are
+      multiplied by 0.1 ln(scale) + 1.
+    """
+    if scaling not in ("none", "linear", "base", "yarn"):
+        raise ValueError(f"scaling {scaling!r}: expected none, linear, base or yarn")
+    if rotary_dim < 2 or rotary_dim % 2 or not base > 0 or not scale > 0 or not original_length > 0:
+        raise ValueError("rotary_dim must be even and positive, base, scale and original_length positive")
+    if scaling == "base" and rotary_dim > 2:
+        base = base * scale ** (rotary_dim / (rotary_dim - 2))
+    freq = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    factor = 1.0
+    if scaling == "linear":
+        freq = freq / scale
+    elif scaling == "yarn":
+        turns = original_length * freq / (2 * math.pi)
+        keep = ((turns - 1) / 31).clamp(0, 1)
+        freq = freq * keep + freq / scale * (1 - keep)
+        factor = 0.1 * math.log(scale) + 1 if scale > 1 else 1.0
+    return Rope(freq.float().to(device), interleaved, factor)
+
+
+def _rows(name: str, t: torch.Tensor, shape, dev: int):
+    """(address, elements from row to row) of q or k [B, T, H, d], heads dense, rows evenly spaced."""
+    B, T, H, d = shape
+    s = t.stride()
+    ok = t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev
+    ok = ok and s[3] == 1 and (H == 1 or s[2] == d)
+    row = s[1] if T > 1 else s[0] if B > 1 else H * d
+    if not (ok and (B == 1 or s[0] == T * row)):
+        raise ValueError(f"{name}: expected a bfloat16 tensor of shape {tuple(shape)} on cuda:{dev} with dense heads and "
+                         f"evenly spaced rows, got {t.dtype} {tuple(t.shape)} with strides {s} on {t.device}")
+    return t.data_ptr(), row
+
+
+def rope(dims: Dims, spec: Rope, q_out, k_out, q, k, start_pos, n_tokens=None, transpose: bool = False,
+         stream=None) -> None:
+    """swa_rope: q [B, T, Hq, d] and k [B, T, Hkv, d] (bf16; heads inside a packed projection are
+    taken as they lie) turned to positions start_pos[b] + t, into dense q_out and k_out (which may be
+    q and k if those are dense).  k and k_out may be None.  ``n_tokens`` None: all T rows.
+    ``transpose`` gives the gradient for q and k from that for q_out and k_out."""
+    dev = _device_of("q", q)
+    if q.dim() != 4 or spec._dev != dev:
+        raise ValueError(f"q: expected [B, T, Hq, d] on cuda:{spec._dev}, got {tuple(q.shape)} on {q.device}")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out: both or neither")
+    B, T, d = dims.batch, int(q.shape[1]), dims.head_dim
+    heads, rows = (B, T, dims.n_q_heads, d), (B, T, dims.n_kv_heads, d)
+    qp, qs = _rows("q", q, heads, dev)
+    kp, ks = _rows("k", k, rows, dev) if k is not None else (None, 0)
+    outs = (_arg("q_out", q_out, heads, torch.bfloat16, dev),
+            _arg("k_out", k_out, rows, torch.bfloat16, dev) if k is not None else None)
+    start = _arg("start_pos", start_pos, (B,), torch.int32, dev)
+    count = _arg("n_tokens", n_tokens, (B,), torch.int32, dev) if n_tokens is not None else None
+    with _on(dev):
+        _check(load_library().swa_rope(ctypes.byref(dims.c()), ctypes.byref(spec._c), *outs, qp, kp, qs, ks, T, start,
+                                       count, int(transpose), _stream_on(stream, dev)))

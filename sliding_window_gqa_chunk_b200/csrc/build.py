@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libswa.so")
 
-SOURCES = ["swa_api.cu", "swa_append.cu", "swa_decode.cu", "swa_prefill.cu", "swa_decode_static.cu"]
+SOURCES = ["swa_api.cu", "swa_append.cu", "swa_decode.cu", "swa_prefill.cu", "swa_decode_static.cu",
+           "swa_q8_api.cu", "swa_q8_cache.cu", "swa_q8_decode.cu", "swa_rope.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -53,7 +54,7 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str | Non
         return LIB
     os.makedirs(os.path.dirname(os.path.abspath(target)), exist_ok=True)
     tmp = target + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "--threads", "0",
            "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
            "-I", INCLUDE, "-I", HERE, "-o", tmp]
     cmd += [f"-D{d}" for d in defines]

@@ -580,6 +580,21 @@ int api_ok() { return ok(); }
 
 int api_status_word(int** out) { return status_ptr(out); }
 
+int api_check_dims(const swa_dims* dims) { return check_dims(dims); }
+
+int api_check_ptrs(const char* names, std::initializer_list<const void*> ptrs) { return check_ptrs(names, ptrs); }
+
+int api_check_ptrs4(const char* names, std::initializer_list<const void*> ptrs) {
+  int i = 0;
+  for (const void* p : ptrs) {
+    if (p == nullptr) return fail(SWA_ERR_INVALID_ARG, "pointer #%d of (%s) is NULL", i, names);
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+      return fail(SWA_ERR_INVALID_ARG, "pointer #%d of (%s) is not 4-byte aligned", i, names);
+    ++i;
+  }
+  return SWA_OK;
+}
+
 int api_check_decode(const swa_dims* dims, const void* out, const void* q, const void* k_new,
                      const void* v_new, const void* k_cache, const void* v_cache, const int32_t* pos) {
   int rc = check_dims(dims);

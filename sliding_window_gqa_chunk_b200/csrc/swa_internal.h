@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 namespace swa {
 
 struct AppendParams {
@@ -119,12 +121,90 @@ cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, int 
 // TMA box width (elements of d per box row) and swizzle span used by the prefill kernel.
 void prefill_map_geometry(int head_dim, int* box_elems, int* swizzle_bytes);
 
+// The 8-bit rolling cache (swa_q8_cache of swa.h): blocks of kQ8Block slots.
+constexpr int kQ8Block = 64;
+
+struct Q8Ring {
+  uint8_t* k8;                  // [B][Hkv][W][d]
+  uint8_t* v8;
+  float* k_scale;               // [B][Hkv][ceil(W / 64)]
+  float* v_scale;
+  __nv_bfloat16* k_tail;        // [B][Hkv][64][d]
+  __nv_bfloat16* v_tail;
+  int format;
+};
+
+struct Q8AppendParams {
+  Q8Ring ring;
+  const __nv_bfloat16* k;       // [B][max_tokens][Hkv][d]
+  const __nv_bfloat16* v;
+  const int32_t* start_pos;     // device [B]
+  const int32_t* n_tokens;
+  int* status;
+  int batch, n_kv_heads, head_dim, window, max_tokens;
+};
+cudaError_t launch_q8_append(const Q8AppendParams& p, cudaStream_t stream);
+
+struct Q8ExpandParams {
+  Q8Ring ring;
+  __nv_bfloat16* k_out;         // [B][Hkv][W][d] bf16: what the ring's rows stand for
+  __nv_bfloat16* v_out;
+  const int32_t* start_pos;
+  const int32_t* n_tokens;
+  int batch, n_kv_heads, head_dim, window, max_tokens;
+};
+cudaError_t launch_q8_expand(const Q8ExpandParams& p, cudaStream_t stream);
+
+struct Q8DecodeParams {
+  Q8Ring ring;
+  void* out;                    // [B][Hq][d] bf16 or f32
+  const __nv_bfloat16* q;       // [B][Hq][d]
+  const __nv_bfloat16* k_new;   // [B][Hkv][d]
+  const __nv_bfloat16* v_new;
+  const int32_t* pos;           // device [B]
+  float* ws_o;                  // [B][Hq][n_splits][d] partial O (two launches)
+  float* ws_ml;                 // [B][Hq][n_splits][2] partial (max, sum)
+  int* status;
+  int batch, n_q_heads, n_kv_heads, head_dim, window;
+  int n_splits, slots_per_split;
+  int warps;                    // warps per CTA
+  int cluster;                  // 1: the splits of a pair merge in a thread-block cluster
+  float scale_log2;             // scale * log2(e)
+  int out_f32;
+};
+// Split of the W slots of one (sequence, kv head); a function of the shape.
+struct Q8DecodeSplit {
+  int n_splits, slots_per_split, warps, cluster;
+};
+Q8DecodeSplit q8_decode_split(int batch, int n_q_heads, int n_kv_heads, int window, int head_dim);
+cudaError_t launch_q8_decode(const Q8DecodeParams& p, cudaStream_t stream);
+
+struct RopeParams {
+  __nv_bfloat16* q_out;         // [B][T][Hq][d]
+  __nv_bfloat16* k_out;         // [B][T][Hkv][d] or NULL
+  const __nv_bfloat16* q;       // rows q_stride elements apart
+  const __nv_bfloat16* k;
+  int64_t q_stride, k_stride;
+  const float* inv_freq;        // device [rotary_dim / 2]
+  const int32_t* start_pos;
+  const int32_t* n_tokens;      // or NULL
+  int* status;
+  int batch, n_q_heads, n_kv_heads, head_dim, max_tokens;
+  int rotary_dim, interleaved;
+  int q_in_place, k_in_place;   // the elements past rotary_dim need no copy
+  float factor, sin_sign;
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+
 // Helpers of the C-ABI layer for entry points defined in other files: set the
 // thread-local error message, look up the device status word, and run the
 // host-side argument checks of a decode call (everything but the workspace).
 int api_fail(int code, const char* fmt, ...);
 int api_ok();
 int api_status_word(int** out);
+int api_check_dims(const struct swa_dims* dims);
+int api_check_ptrs(const char* names, std::initializer_list<const void*> ptrs);      // 16-byte aligned
+int api_check_ptrs4(const char* names, std::initializer_list<const void*> ptrs);     // 4-byte aligned
 int api_check_decode(const struct swa_dims* dims, const void* out, const void* q, const void* k_new,
                      const void* v_new, const void* k_cache, const void* v_cache, const int32_t* pos);
 

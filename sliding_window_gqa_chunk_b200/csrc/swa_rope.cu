@@ -1,0 +1,146 @@
+// swa_rope.cu - rotary positions: the first r elements of each head's row are
+// pairs, and the pair i of the row at position p is turned by p * inv_freq[i].
+//
+// Pure streaming: every row is read and written once, so the bound is HBM for
+// chunks and the launch for a decode step.  The angles of a token are the same
+// for all its heads: the CTA computes the cos and sin of its tokens once into
+// shared memory, and each thread keeps those of its 8 pairs in registers
+// while it goes through its share of the heads.  A thread's unit is 16
+// elements of a head, two 16-byte pieces that hold whole pairs: [8c, 8c + 8)
+// and [r/2 + 8c, ...) with halves, [16c, 16c + 16) interleaved; pair 8c + i is
+// the i-th of unit c either way.
+//
+// The angle is p * f in fp64, brought to a fraction of a turn there, and only
+// then rounded to fp32: p * f in fp32 would be off by half a radian at
+// positions above 2^23.
+#include "swa_common.cuh"
+#include "swa_internal.h"
+
+namespace swa {
+
+namespace {
+constexpr int kThreads = 256;
+constexpr int kTokens = 4;          // tokens of a CTA in a chunk
+constexpr int kMaxPairs = 64;       // rotary_dim <= 128
+
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Turns the 8 pairs of a unit.  INTER: the pairs lie side by side in (a, b),
+// else pair i is element i of a and of b.
+template <bool INTER>
+__device__ __forceinline__ void turn(uint4& a, uint4& b, const float (&cs)[8], const float (&sn)[8]) {
+  uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  if constexpr (INTER) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = lo(x[i]), v = hi(x[i]);
+      x[i] = pack_bf16x2(u * cs[i] - v * sn[i], v * cs[i] + u * sn[i]);
+      const float w = lo(y[i]), z = hi(y[i]);
+      y[i] = pack_bf16x2(w * cs[4 + i] - z * sn[4 + i], z * cs[4 + i] + w * sn[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u0 = lo(x[i]), u1 = hi(x[i]), v0 = lo(y[i]), v1 = hi(y[i]);
+      x[i] = pack_bf16x2(u0 * cs[2 * i] - v0 * sn[2 * i], u1 * cs[2 * i + 1] - v1 * sn[2 * i + 1]);
+      y[i] = pack_bf16x2(v0 * cs[2 * i] + u0 * sn[2 * i], v1 * cs[2 * i + 1] + u1 * sn[2 * i + 1]);
+    }
+  }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
+  b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+}  // namespace
+
+// TOK tokens (of all B * T, numbered through) per CTA.
+template <bool INTER, int TOK>
+__global__ void __launch_bounds__(kThreads) swa_rope_kernel(const RopeParams p) {
+  __shared__ float2 ang[TOK][kMaxPairs];
+  __shared__ int live[TOK];
+  wait_prior_grid();
+  allow_next_grid();
+  const int T = p.max_tokens, r2 = p.rotary_dim / 2;
+  const int first = blockIdx.x * TOK;
+  const int n_rows = p.batch * T;                     // below 2^31
+  for (int i = threadIdx.x; i < TOK * r2; i += kThreads) {
+    const int tok = first + i / r2, pair = i % r2;
+    bool ok = false;
+    if (tok < n_rows) {
+      const int b = tok / T, t = tok - b * T;
+      const int s = p.start_pos[b], n = p.n_tokens != nullptr ? p.n_tokens[b] : T;
+      if (s < 0 || n < 0 || n > T) {
+        if (t == 0 && pair == 0) raise_status(p.status, SWA_ERR_DEVICE_ARG);
+      } else if (t < n) {
+        ok = true;
+        const double turns = (double)((long long)s + t) * (double)p.inv_freq[pair] * 0.15915494309189535;
+        float sn, cs;
+        sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
+        ang[i / r2][pair] = make_float2(cs * p.factor, sn * p.factor * p.sin_sign);
+      }
+    }
+    if (pair == 0) live[i / r2] = ok;
+  }
+  __syncthreads();
+
+  // thread -> (unit c of a row, token, first head); the heads go in steps
+  const int units = p.head_dim / 16;                  // 1, 4 or 8: divides the threads
+  const int c = threadIdx.x % units;
+  const int tk = threadIdx.x / units % TOK;
+  const int lane = threadIdx.x / (units * TOK);
+  const int lanes = kThreads / (units * TOK);
+  if (!live[tk]) return;
+  const int tok = first + tk;
+  const int rot = p.rotary_dim / 16;                  // units that are turned
+  const bool turned = c < rot;
+  float cs[8], sn[8];
+  if (turned) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 a = ang[tk][8 * c + i];
+      cs[i] = a.x;
+      sn[i] = a.y;
+    }
+  }
+  // first elements of the unit's two pieces
+  const int e0 = (!INTER && turned) ? 8 * c : 16 * c;
+  const int e1 = (!INTER && turned) ? p.rotary_dim / 2 + 8 * c : 16 * c + 8;
+  const int heads = p.n_q_heads + p.n_kv_heads;
+  for (int h = blockIdx.y * lanes + lane; h < heads; h += gridDim.y * lanes) {
+    const bool is_q = h < p.n_q_heads;
+    if (!turned && (is_q ? p.q_in_place : p.k_in_place)) continue;
+    const int hh = is_q ? h : h - p.n_q_heads;
+    const __nv_bfloat16* src = (is_q ? p.q + tok * p.q_stride : p.k + tok * p.k_stride) + (size_t)hh * p.head_dim;
+    __nv_bfloat16* dst = (is_q ? p.q_out + (size_t)tok * p.n_q_heads * p.head_dim
+                               : p.k_out + (size_t)tok * p.n_kv_heads * p.head_dim) + (size_t)hh * p.head_dim;
+    uint4 a = *reinterpret_cast<const uint4*>(src + e0), b = *reinterpret_cast<const uint4*>(src + e1);
+    if (turned) turn<INTER>(a, b, cs, sn);
+    *reinterpret_cast<uint4*>(dst + e0) = a;
+    *reinterpret_cast<uint4*>(dst + e1) = b;
+  }
+}
+
+namespace {
+template <bool INTER, int TOK>
+cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t stream) {
+  const long long rows = (long long)p.batch * p.max_tokens;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + TOK - 1) / TOK));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, swa_rope_kernel<INTER, TOK>, p);
+}
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
+  // one token per CTA until that fills the SMs several times over
+  if ((long long)p.batch * p.max_tokens < 148 * 8)
+    return p.interleaved ? launch_rope_t<true, 1>(p, stream) : launch_rope_t<false, 1>(p, stream);
+  return p.interleaved ? launch_rope_t<true, kTokens>(p, stream) : launch_rope_t<false, kTokens>(p, stream);
+}
+
+}  // namespace swa
