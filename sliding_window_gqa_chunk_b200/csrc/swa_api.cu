@@ -140,15 +140,16 @@ int get_encode(EncodeTiledFn* fn) {
   return SWA_OK;
 }
 
-// rank-`rank` bf16 map, dims innermost first, byte strides of dims 1..rank-1.
+// rank-`rank` map (bf16 unless given), dims innermost first, byte strides of dims 1..rank-1.
 int encode_map(EncodeTiledFn fn, CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims,
-               const cuuint64_t* strides, const cuuint32_t* box, int swizzle_bytes, const char* what) {
+               const cuuint64_t* strides, const cuuint32_t* box, int swizzle_bytes, const char* what,
+               CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   cuuint32_t estride[5] = {1, 1, 1, 1, 1};
   CUtensorMapSwizzle swz = swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                            : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                            : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                  : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims,
+  CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void*>(ptr), dims,
                   strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what, (int)r);
@@ -579,6 +580,17 @@ int api_fail(int code, const char* fmt, ...) {
 int api_ok() { return ok(); }
 
 int api_status_word(int** out) { return status_ptr(out); }
+
+int api_encode_bytes(CUtensorMap* map, const void* ptr, int row_bytes, int rows, long long n, int box_rows,
+                     const char* what) {
+  EncodeTiledFn enc = nullptr;
+  const int rc = get_encode(&enc);
+  if (rc) return rc;
+  const cuuint64_t dims3[3] = {(cuuint64_t)row_bytes, (cuuint64_t)rows, (cuuint64_t)n};
+  const cuuint64_t str3[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows * row_bytes};
+  const cuuint32_t box3[3] = {(cuuint32_t)row_bytes, (cuuint32_t)box_rows, 1};
+  return encode_map(enc, map, ptr, 3, dims3, str3, box3, row_bytes, what, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
 
 int api_check_dims(const swa_dims* dims) { return check_dims(dims); }
 

@@ -177,7 +177,13 @@ struct Q8DecodeSplit {
   int n_splits, slots_per_split, warps, cluster;
 };
 Q8DecodeSplit q8_decode_split(int batch, int n_q_heads, int n_kv_heads, int window, int head_dim);
-cudaError_t launch_q8_decode(const Q8DecodeParams& p, cudaStream_t stream);
+// TMA descriptors of the ring's keys and values: [B * Hkv][W][d] bytes, boxes of
+// q8_decode_box_rows() rows, swizzled by the row's size.
+struct Q8DecodeMaps {
+  CUtensorMap k, v;
+};
+int q8_decode_box_rows();
+cudaError_t launch_q8_decode(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream);
 
 struct RopeParams {
   __nv_bfloat16* q_out;         // [B][T][Hq][d]
@@ -202,6 +208,9 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 int api_fail(int code, const char* fmt, ...);
 int api_ok();
 int api_status_word(int** out);
+// Encodes a descriptor of bytes [n][rows][row_bytes] with boxes of box_rows whole rows.
+int api_encode_bytes(CUtensorMap* map, const void* ptr, int row_bytes, int rows, long long n, int box_rows,
+                     const char* what);
 int api_check_dims(const struct swa_dims* dims);
 int api_check_ptrs(const char* names, std::initializer_list<const void*> ptrs);      // 16-byte aligned
 int api_check_ptrs4(const char* names, std::initializer_list<const void*> ptrs);     // 4-byte aligned

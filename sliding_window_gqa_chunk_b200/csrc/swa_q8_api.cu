@@ -180,7 +180,12 @@ int swa_q8_decode(const swa_dims* dims, void* out, const void* q, const void* k_
   p.cluster = sp.cluster;
   p.scale_log2 = dims->scale * 1.4426950408889634f;
   p.out_f32 = dims->out_dtype == SWA_DTYPE_F32;
-  const cudaError_t e = swa::launch_q8_decode(p, static_cast<cudaStream_t>(stream));
+  swa::Q8DecodeMaps maps;
+  const long long pairs = (long long)dims->batch * dims->n_kv_heads;
+  const int box = swa::q8_decode_box_rows();
+  if ((rc = swa::api_encode_bytes(&maps.k, cache->k, dims->head_dim, dims->window, pairs, box, "cache k"))) return rc;
+  if ((rc = swa::api_encode_bytes(&maps.v, cache->v, dims->head_dim, dims->window, pairs, box, "cache v"))) return rc;
+  const cudaError_t e = swa::launch_q8_decode(p, maps, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "swa_q8_decode");
   return swa::api_ok();
 }

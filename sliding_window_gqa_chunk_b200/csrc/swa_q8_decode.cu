@@ -41,6 +41,7 @@
 #include "swa_common.cuh"
 #include "swa_internal.h"
 #include "swa_q8.cuh"
+#include "swa_tc.cuh"
 
 namespace swa {
 
@@ -58,22 +59,41 @@ struct Q8Frag {
   static constexpr int kMTiles = D / 16;
 };
 
+// Tiles in shared memory lie as TMA writes them: rows of D bytes whose 16-byte
+// pieces are permuted (128-byte swizzle for d = 128: piece ^ (row & 7), 64-byte
+// swizzle for d = 64: piece ^ (row / 2 & 3)), so that the lanes of a load fall on
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  if constexpr (D == 128) return row * 128 + ((piece ^ (row & 7)) << 4);
+  if constexpr (D == 64) return row * 64 + ((piece ^ (row >> 1 & 3)) << 4);
+  return row * 16;
+}
+
 // First element of lane-quad t's key word w.  Dot products do not depend on
-// the order of d, so the order that gives 16-byte loads is used for K and Q.
+// the order of d; this one reads whole pieces, and with the swizzle above the
+// two rows and four pieces of 8 lanes fall on all 32 banks.
 template <int D>
 __device__ __forceinline__ int key_elem(int t, int w) {
   if constexpr (D == 16) return 4 * t;
-  return (w / 4) * 64 + t * 16 + (w % 4) * 4;
+  if constexpr (D == 64) return 16 * t + 4 * w;
+  return (2 * t + w / 4) * 16 + (w % 4) * 4;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
 }
 
 template <int D>
-__device__ __forceinline__ void load_key8(uint32_t (&w)[Q8Frag<D>::kKWords], const uint8_t* row, int t, bool valid) {
+__device__ __forceinline__ void load_key8(uint32_t (&w)[Q8Frag<D>::kKWords], uint32_t tile, int row, int t) {
   if constexpr (D == 16) {
-    w[0] = valid ? ldg_stream4(row + 4 * t) : 0u;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(tile + row * 16 + 4 * t));
   } else {
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
-      const uint4 x = valid ? ldg_stream(row + j * 64 + t * 16) : make_uint4(0, 0, 0, 0);
+      const uint4 x = lds128(tile + piece_at<D>(row, (D / 64) * t + j));
       w[4 * j] = x.x;
       w[4 * j + 1] = x.y;
       w[4 * j + 2] = x.z;
@@ -84,15 +104,17 @@ __device__ __forceinline__ void load_key8(uint32_t (&w)[Q8Frag<D>::kKWords], con
 
 // Lane-group g's values: elements [g D / 8, (g + 1) D / 8) of a row.
 template <int D>
-__device__ __forceinline__ void load_val8(uint32_t (&w)[Q8Frag<D>::kVWords], const uint8_t* row, int g, bool valid) {
+__device__ __forceinline__ void load_val8(uint32_t (&w)[Q8Frag<D>::kVWords], uint32_t tile, int row, int g) {
   if constexpr (D == 16) {
-    w[0] = valid ? (uint32_t)*reinterpret_cast<const uint16_t*>(row + 2 * g) : 0u;
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(tile + row * 16 + 2 * g));
+    w[0] = x;
   } else if constexpr (D == 64) {
-    const uint2 x = valid ? ldg_stream8(row + 8 * g) : make_uint2(0, 0);
-    w[0] = x.x;
-    w[1] = x.y;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(w[0]), "=r"(w[1])
+                 : "r"(tile + piece_at<D>(row, g >> 1) + (g & 1) * 8));
   } else {
-    const uint4 x = valid ? ldg_stream(row + 16 * g) : make_uint4(0, 0, 0, 0);
+    const uint4 x = lds128(tile + piece_at<D>(row, g));
     w[0] = x.x;
     w[1] = x.y;
     w[2] = x.z;
@@ -131,8 +153,19 @@ __device__ __forceinline__ int f16_exp(uint32_t amax) {
 template <int D>
 constexpr int q8_o_stride() { return D + 1; }
 template <int D, int NT, int NW>
+constexpr int q8_merge_bytes() {
+  return (int)sizeof(float) * (NW * 8 * NT * (2 + q8_o_stride<D>()) + 8 * NT * (2 + D));
+}
+// Shared memory: the warps' rings (the merge reuses them), 2 words, barriers, and
+// what it takes to start on a 1024-byte boundary (the swizzle goes by the address).
+template <int D, int NT, int NW, int SUB, int R>
+constexpr int q8_ring_bytes() {
+  constexpr int ring = NW * R * SUB * kSub * D, merge = q8_merge_bytes<D, NT, NW>();
+  return ((ring > merge ? ring : merge) + 15) / 16 * 16;
+}
+template <int D, int NT, int NW, int SUB, int R>
 constexpr int q8_smem_bytes() {
-  return (int)sizeof(float) * (NW * 8 * NT * (2 + q8_o_stride<D>()) + 8 * NT * (2 + D)) + 16;
+  return 1024 + q8_ring_bytes<D, NT, NW, SUB, R>() + 16 + NW * R * 8;
 }
 
 __device__ __forceinline__ void store_out(void* out, size_t i, float x, int f32) {
@@ -182,30 +215,52 @@ __device__ __forceinline__ void softmax_step(State<D>& st, float (&x)[SUB][4], i
   }
   st.l[0] = st.l[0] * a0 + s0 * inv;
   st.l[1] = st.l[1] * a1 + s1 * inv;
+  if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {   // a maximum moved
 #pragma unroll
-  for (int mt = 0; mt < Q8Frag<D>::kMTiles; ++mt) {
-    st.o[mt][0] *= a0;
-    st.o[mt][1] *= a1;
-    st.o[mt][2] *= a0;
-    st.o[mt][3] *= a1;
+    for (int mt = 0; mt < Q8Frag<D>::kMTiles; ++mt) {
+      st.o[mt][0] *= a0;
+      st.o[mt][1] *= a1;
+      st.o[mt][2] *= a0;
+      st.o[mt][3] *= a1;
+    }
   }
 }
 
 }  // namespace
 
 // NT = number of 8-head n-tiles (ceil(G / 8)); NW = warps; SUB = 16-slot
-// blocks that a warp takes at a time.
-template <int D, int NT, int NW, int SUB, int FMT>
-__global__ void __launch_bounds__(NW * 32) swa_q8_decode_kernel(const Q8DecodeParams p) {
+// blocks that a warp takes at a time; R = tiles (keys or values of a piece) in
+// a warp's ring.
+template <int D, int NT, int NW, int SUB, int R, int FMT>
+__global__ void __launch_bounds__(NW * 32)
+swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
   using F = Q8Frag<D>;
   constexpr int kPiece = kSub * SUB;
-  extern __shared__ __align__(16) float smem[];
+  constexpr int kTile = kPiece * D;
+  static_assert(kQ8Block % kPiece == 0, "a piece has one scale");
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem_al = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024;
+  float* smem = reinterpret_cast<float*>(smem_al);
 
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.n_q_heads / p.n_kv_heads;
   const int W = p.window;
+
+  // each warp streams its own pieces: tiles K0 V0 K1 V1 ... through a ring of R,
+  // one barrier a place, filled by TMA and freed by the warp itself
+  const uint32_t ring = tc::smem_u32(smem_al) + warp * R * kTile;
+  const uint32_t bars = tc::smem_u32(smem_al) + q8_ring_bytes<D, NT, NW, SUB, R>() + 16 + warp * R * 8;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) tc::mbar_init(bars + 8 * i, 1);
+    tc::mbar_fence_init();
+    tc::prefetch_map(&k_map);
+    tc::prefetch_map(&v_map);
+  }
+  __syncwarp();
 
   wait_prior_grid();
   allow_next_grid();
@@ -225,14 +280,40 @@ __global__ void __launch_bounds__(NW * 32) swa_q8_decode_kernel(const Q8DecodePa
 
   const size_t unit = (size_t)b * p.n_kv_heads + kvh;
   const int n_blocks = (W + kQ8Block - 1) / kQ8Block;
-  const uint8_t* kc = p.ring.k8 + unit * W * D;
-  const uint8_t* vc = p.ring.v8 + unit * W * D;
   const float* ksc = p.ring.k_scale + unit * n_blocks;
   const float* vsc = p.ring.v_scale + unit * n_blocks;
   __nv_bfloat16* kt = p.ring.k_tail + unit * kQ8Block * D;
   __nv_bfloat16* vt = p.ring.v_tail + unit * kQ8Block * D;
   const __nv_bfloat16* kn = p.k_new + unit * D;
   const __nv_bfloat16* vn = p.v_new + unit * D;
+
+  // rows [first_row(x), r_end) of the piece at slot x are held in 8 bits and in the window
+  auto first_row = [&](int x) { return (x >= blk0 && x <= s_new) ? s_new + 1 : x; };
+  auto next_piece = [&](int x) {
+    do x += NW * kPiece;
+    while (x < r_end && first_row(x) >= min(x + kPiece, r_end));
+    return x;
+  };
+  // the tile after the last one issued: piece, whether its values, place in the ring
+  int is_x = next_piece(r_begin + warp * kPiece - NW * kPiece), is_v = 0, is_at = 0;
+  auto issue = [&]() {
+    if (is_x >= r_end) return;
+    if (lane == 0) {
+      tc::mbar_arrive_expect_tx(bars + 8 * is_at, kTile);
+      tc::tma_load_3d(ring + is_at * kTile, is_v ? &v_map : &k_map, 0, is_x, (int)unit, bars + 8 * is_at);
+    }
+    if (is_v) is_x = next_piece(is_x);
+    is_v ^= 1;
+    is_at = is_at + 1 == R ? 0 : is_at + 1;
+  };
+  int x0 = is_x;
+#pragma unroll
+  for (int i = 0; i < R; ++i) issue();
+  float ks = 0.f, vs = 1.f;
+  if (x0 < r_end) {
+    ks = ksc[x0 / kQ8Block];
+    vs = vsc[x0 / kQ8Block];
+  }
 
   // Q as the B operand of S^T = K Q^T, f16: lane (g, t) holds head 8 nt + g.
   uint32_t qf[NT][2 * F::kKWords];
@@ -271,85 +352,15 @@ __global__ void __launch_bounds__(NW * 32) swa_q8_decode_kernel(const Q8DecodePa
     for (int mt = 0; mt < F::kMTiles; ++mt) st[nt].o[mt][0] = st[nt].o[mt][1] = st[nt].o[mt][2] = st[nt].o[mt][3] = 0.f;
   }
 
-  for (int x0 = r_begin + warp * kPiece; x0 < r_end; x0 += NW * kPiece) {
-    // rows [lo, hi) of the piece are held in 8 bits and in the window
-    const int lo = (x0 >= blk0 && x0 <= s_new) ? s_new + 1 : x0;
-    const int hi = x0 + kPiece < r_end ? x0 + kPiece : r_end;
-    if (lo >= hi) continue;
-    uint32_t kw[SUB][2][F::kKWords];
-    uint32_t vw[SUB][4][F::kVWords];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = x0 + u * kSub + i * 8 + g;
-        load_key8<D>(kw[u][i], kc + (size_t)r * D, t, r >= lo && r < hi);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = x0 + u * kSub + 2 * t + (i & 1) + (i >> 1) * 8;
-        load_val8<D>(vw[u][i], vc + (size_t)r * D, g, r >= lo && r < hi);
-      }
-    }
-    const float ks = ksc[x0 / kQ8Block];
-    const int ve = q8::exp_of(vsc[x0 / kQ8Block]);
-
-    uint32_t pb[NT][SUB][2];
-    float x[NT][SUB][4];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt][u][0] = x[nt][u][1] = x[nt][u][2] = x[nt][u][3] = 0.f;
-#pragma unroll
-      for (int w = 0; w < F::kKWords; ++w) {
-        uint32_t a0, a1, a2, a3;
-        q8::unpack4<FMT>(kw[u][0][w], a0, a2);
-        q8::unpack4<FMT>(kw[u][1][w], a1, a3);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt][u], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float f0 = qs[nt][0] * ks, f1 = qs[nt][1] * ks;
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        const int r0 = x0 + u * kSub + g, r1 = r0 + 8;
-        const bool ok0 = r0 >= lo && r0 < hi, ok1 = r1 >= lo && r1 < hi;
-        x[nt][u][0] = ok0 ? x[nt][u][0] * f0 : -CUDART_INF_F;
-        x[nt][u][1] = ok0 ? x[nt][u][1] * f1 : -CUDART_INF_F;
-        x[nt][u][2] = ok1 ? x[nt][u][2] * f0 : -CUDART_INF_F;
-        x[nt][u][3] = ok1 ? x[nt][u][3] * f1 : -CUDART_INF_F;
-      }
-      softmax_step<D, SUB>(st[nt], x[nt], ve, pb[nt]);
-    }
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-      for (int mt = 0; mt < F::kMTiles; ++mt) {
-        // bytes 2 mt, 2 mt + 1 of rows (2t, 2t + 1) and (2t + 8, 2t + 9), paired by element
-        const uint32_t sel = (mt & 1) ? 0x7362 : 0x5140;
-        uint32_t a0, a1, a2, a3;
-        q8::unpack4<FMT>(prmt(vw[u][0][mt / 2], vw[u][1][mt / 2], sel), a0, a1);
-        q8::unpack4<FMT>(prmt(vw[u][2][mt / 2], vw[u][3][mt / 2], sel), a2, a3);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(st[nt].o[mt], a0, a1, a2, a3, pb[nt][u][0], pb[nt][u][1]);
-      }
-    }
-  }
-
   if (owner) {
     // rows 0 .. row_new of the block being filled, 16 at a time: rows before
     // row_new from the tail, row_new from k_new / v_new
-    for (int x0 = warp * kSub; x0 <= row_new; x0 += NW * kSub) {
+    for (int y0 = warp * kSub; y0 <= row_new; y0 += NW * kSub) {
       uint32_t kw[2][2 * F::kKWords], vw[4][F::kMTiles];
       uint32_t km = 0, vm = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = x0 + i * 8 + g;
+        const int r = y0 + i * 8 + g;
         const __nv_bfloat16* row = r == row_new ? kn : kt + (size_t)r * D;
 #pragma unroll
         for (int w = 0; w < F::kKWords; ++w) {
@@ -361,7 +372,7 @@ __global__ void __launch_bounds__(NW * 32) swa_q8_decode_kernel(const Q8DecodePa
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = x0 + 2 * t + (i & 1) + (i >> 1) * 8;
+        const int r = y0 + 2 * t + (i & 1) + (i >> 1) * 8;
         const __nv_bfloat16* row = r == row_new ? vn : vt + (size_t)r * D;
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt) {
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(NW * 32) swa_q8_decode_kernel(const Q8DecodePa
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt) vw[i][mt] = bf16_to_f16(vw[i][mt], vf);
-      const bool ok0 = x0 + g <= row_new, ok1 = x0 + 8 + g <= row_new;
+      const bool ok0 = y0 + g <= row_new, ok1 = y0 + 8 + g <= row_new;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
@@ -403,8 +414,108 @@ __global__ void __launch_bounds__(NW * 32) swa_q8_decode_kernel(const Q8DecodePa
     }
   }
 
+  bool ok = true;
+  int at = 0, phase = 0;                       // place and phase of the next tile to read
+  while (x0 < r_end) {
+    const int lo = first_row(x0), hi = x0 + kPiece < r_end ? x0 + kPiece : r_end;
+    const int x1 = next_piece(x0);
+    float ks1 = 0.f, vs1 = 1.f;                // the next piece's scales, a piece ahead
+    if (x1 < r_end) {
+      ks1 = ksc[x1 / kQ8Block];
+      vs1 = vsc[x1 / kQ8Block];
+    }
+    const int ve = q8::exp_of(vs);
+
+    if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, phase, p.status)))) break;
+    uint32_t tile = ring + at * kTile;
+    float x[NT][SUB][4];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      uint32_t kw[2][F::kKWords];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_key8<D>(kw[i], tile, u * kSub + i * 8 + g, t);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt][u][0] = x[nt][u][1] = x[nt][u][2] = x[nt][u][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < F::kKWords; ++w) {
+        uint32_t a0, a1, a2, a3;
+        q8::unpack4<FMT>(kw[0][w], a0, a2);
+        q8::unpack4<FMT>(kw[1][w], a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt][u], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+      }
+    }
+    __syncwarp();
+    issue();                                   // into the place of the keys just read
+    if (++at == R) at = 0, phase ^= 1;
+
+    const bool partial = lo > x0 || hi < x0 + kPiece;
+    uint32_t pb[NT][SUB][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float f0 = qs[nt][0] * ks, f1 = qs[nt][1] * ks;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        x[nt][u][0] *= f0;
+        x[nt][u][1] *= f1;
+        x[nt][u][2] *= f0;
+        x[nt][u][3] *= f1;
+      }
+      if (partial) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const int r0 = x0 + u * kSub + g, r1 = r0 + 8;
+          if (r0 < lo || r0 >= hi) x[nt][u][0] = x[nt][u][1] = -CUDART_INF_F;
+          if (r1 < lo || r1 >= hi) x[nt][u][2] = x[nt][u][3] = -CUDART_INF_F;
+        }
+      }
+      softmax_step<D, SUB>(st[nt], x[nt], ve, pb[nt]);
+    }
+
+    if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, phase, p.status)))) break;
+    tile = ring + at * kTile;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      uint32_t vw[4][F::kVWords];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = u * kSub + 2 * t + (i & 1) + (i >> 1) * 8;
+        load_val8<D>(vw[i], tile, r, g);
+        if (partial && (x0 + r < lo || x0 + r >= hi)) {   // 0 times what the row holds must be 0
+#pragma unroll
+          for (int w = 0; w < F::kVWords; ++w) vw[i][w] = 0;
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < F::kMTiles; ++mt) {
+        // bytes 2 mt, 2 mt + 1 of rows (2t, 2t + 1) and (2t + 8, 2t + 9), paired by element
+        const uint32_t sel = (mt & 1) ? 0x7362 : 0x5140;
+        uint32_t a0, a1, a2, a3;
+        q8::unpack4<FMT>(prmt(vw[0][mt / 2], vw[1][mt / 2], sel), a0, a1);
+        q8::unpack4<FMT>(prmt(vw[2][mt / 2], vw[3][mt / 2], sel), a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(st[nt].o[mt], a0, a1, a2, a3, pb[nt][u][0], pb[nt][u][1]);
+      }
+    }
+    __syncwarp();
+    issue();
+    if (++at == R) at = 0, phase ^= 1;
+    x0 = x1;
+    ks = ks1;
+    vs = vs1;
+  }
+  if (!ok) {
+    // a wait ran out (raised in the status word): give every copy still in flight its time to land
+    for (int i = 0; i < R; ++i) {
+      tc::mbar_wait(bars + 8 * at, phase, p.status);
+      if (++at == R) at = 0, phase ^= 1;
+    }
+  }
+
   // ---- merge the NW warps of the CTA ----
-  // smem: m[NW][G8], l[NW][G8], O[NW][G8][kOS], then the CTA's m[G8], l[G8], O[G8][D]
+  // smem (the rings, once every warp is done with its own): m[NW][G8], l[NW][G8], O[NW][G8][kOS], then
+  // the CTA's m[G8], l[G8], O[G8][D]
+  __syncthreads();
   constexpr int G8 = 8 * NT;
   constexpr int kOS = q8_o_stride<D>();
   float* sm_m = smem;
@@ -413,7 +524,7 @@ __global__ void __launch_bounds__(NW * 32) swa_q8_decode_kernel(const Q8DecodePa
   float* cta_m = sm_o + (size_t)NW * G8 * kOS;
   float* cta_l = cta_m + G8;
   float* cta_o = cta_l + G8;
-  uint32_t* red = reinterpret_cast<uint32_t*>(cta_o + G8 * D);
+  uint32_t* red = reinterpret_cast<uint32_t*>(smem_al + q8_ring_bytes<D, NT, NW, SUB, R>());
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float l0 = st[nt].l[0], l1 = st[nt].l[1];
@@ -555,10 +666,10 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-template <int D, int NT, int NW, int SUB, int FMT>
-cudaError_t launch_t(const Q8DecodeParams& p, cudaStream_t stream) {
-  constexpr int smem = q8_smem_bytes<D, NT, NW>();
-  auto kern = swa_q8_decode_kernel<D, NT, NW, SUB, FMT>;
+template <int D, int NT, int NW, int SUB, int R, int FMT>
+cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
+  constexpr int smem = q8_smem_bytes<D, NT, NW, SUB, R>();
+  auto kern = swa_q8_decode_kernel<D, NT, NW, SUB, R, FMT>;
   if (smem > 48 * 1024) {
     // raised once per device (the attribute persists for the process)
     static bool set[kMaxDevices] = {};
@@ -586,7 +697,7 @@ cudaError_t launch_t(const Q8DecodeParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster ? 2 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, maps.k, maps.v);
   if (e != cudaSuccess || p.n_splits == 1 || p.cluster) return e;
   cudaLaunchConfig_t ccfg = {};
   ccfg.gridDim = dim3((unsigned)((size_t)p.batch * p.n_q_heads));
@@ -597,17 +708,29 @@ cudaError_t launch_t(const Q8DecodeParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&ccfg, swa_q8_decode_combine_kernel<D>, p);
 }
 
+#ifndef Q8_SUB
+#define Q8_SUB 2
+#endif
+#ifndef Q8_R4
+#define Q8_R4 3
+#endif
+#ifndef Q8_R8
+#define Q8_R8 3
+#endif
 template <int D, int FMT>
-cudaError_t launch_f(const Q8DecodeParams& p, cudaStream_t stream) {
+cudaError_t launch_f(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
   const bool wide = p.n_q_heads / p.n_kv_heads > 8;
   if (p.warps == 8)
-    return wide ? launch_t<D, 2, 8, 1, FMT>(p, stream) : launch_t<D, 1, 8, 1, FMT>(p, stream);
-  return wide ? launch_t<D, 2, 4, 1, FMT>(p, stream) : launch_t<D, 1, 4, 1, FMT>(p, stream);
+    return wide ? launch_t<D, 2, 8, Q8_SUB, Q8_R8, FMT>(p, maps, stream)
+                : launch_t<D, 1, 8, Q8_SUB, Q8_R8, FMT>(p, maps, stream);
+  return wide ? launch_t<D, 2, 4, Q8_SUB, Q8_R4, FMT>(p, maps, stream)
+              : launch_t<D, 1, 4, Q8_SUB, Q8_R4, FMT>(p, maps, stream);
 }
 
 template <int D>
-cudaError_t launch_d(const Q8DecodeParams& p, cudaStream_t stream) {
-  return p.ring.format == SWA_Q8_E4M3 ? launch_f<D, SWA_Q8_E4M3>(p, stream) : launch_f<D, SWA_Q8_INT8>(p, stream);
+cudaError_t launch_d(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
+  return p.ring.format == SWA_Q8_E4M3 ? launch_f<D, SWA_Q8_E4M3>(p, maps, stream)
+                                      : launch_f<D, SWA_Q8_INT8>(p, maps, stream);
 }
 
 }  // namespace
@@ -636,11 +759,13 @@ Q8DecodeSplit q8_decode_split(int batch, int n_q_heads, int n_kv_heads, int wind
   return s;
 }
 
-cudaError_t launch_q8_decode(const Q8DecodeParams& p, cudaStream_t stream) {
+int q8_decode_box_rows() { return Q8_SUB * kSub; }
+
+cudaError_t launch_q8_decode(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
   switch (p.head_dim) {
-    case 16: return launch_d<16>(p, stream);
-    case 64: return launch_d<64>(p, stream);
-    case 128: return launch_d<128>(p, stream);
+    case 16: return launch_d<16>(p, maps, stream);
+    case 64: return launch_d<64>(p, maps, stream);
+    case 128: return launch_d<128>(p, maps, stream);
   }
   return cudaErrorInvalidValue;
 }
