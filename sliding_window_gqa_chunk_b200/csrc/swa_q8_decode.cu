@@ -48,6 +48,10 @@ namespace swa {
 namespace {
 
 constexpr int kSub = 16;            // slots of one mma block
+constexpr int kSubs = kQ8Block / kSub;        // mma blocks of a scale block
+constexpr int kTileRows = 32;       // rows of a TMA tile
+constexpr int kTileSubs = kTileRows / kSub;
+constexpr int kTiles = kQ8Block / kTileRows;  // tiles of a block's keys (and of its values)
 constexpr int kMaxCluster = 8;      // portable cluster size
 
 // Row fragments of a lane: bytes of a key row (D / 4) and of a value row (D / 8).
@@ -83,6 +87,17 @@ __device__ __forceinline__ int key_elem(int t, int w) {
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
 
@@ -152,20 +167,24 @@ __device__ __forceinline__ int f16_exp(uint32_t amax) {
 
 template <int D>
 constexpr int q8_o_stride() { return D + 1; }
+// Shared memory of the merge: m, l and O of each warp (in the rings, once every warp is
+// done with its own), and what the CTAs of a cluster send to one another.
 template <int D, int NT, int NW>
 constexpr int q8_merge_bytes() {
-  return (int)sizeof(float) * (NW * 8 * NT * (2 + q8_o_stride<D>()) + 8 * NT * (2 + D));
+  return (int)sizeof(float) * NW * 8 * NT * (2 + q8_o_stride<D>());
 }
-// Shared memory: the warps' rings (the merge reuses them), 2 words, barriers, and
-// what it takes to start on a 1024-byte boundary (the swizzle goes by the address).
-template <int D, int NT, int NW, int SUB, int R>
+template <int D, int NT>
+constexpr int q8_peer_floats() { return kMaxCluster * 8 * NT * 2 + 8 * NT * D + kMaxCluster; }
+template <int D, int NT, int NW, int R>
 constexpr int q8_ring_bytes() {
-  constexpr int ring = NW * R * SUB * kSub * D, merge = q8_merge_bytes<D, NT, NW>();
+  constexpr int ring = NW * R * kTileRows * D, merge = q8_merge_bytes<D, NT, NW>();
   return ((ring > merge ? ring : merge) + 15) / 16 * 16;
 }
-template <int D, int NT, int NW, int SUB, int R>
+// All of it: rings, 2 words, barriers, the peers' part, and what it takes to start on a
+// 1024-byte boundary (the swizzle goes by the address).
+template <int D, int NT, int NW, int R>
 constexpr int q8_smem_bytes() {
-  return 1024 + q8_ring_bytes<D, NT, NW, SUB, R>() + 16 + NW * R * 8;
+  return 1024 + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8 + 4 * q8_peer_floats<D, NT>();
 }
 
 __device__ __forceinline__ void store_out(void* out, size_t i, float x, int f32) {
@@ -182,10 +201,16 @@ struct State {
   float o[Q8Frag<D>::kMTiles][4];
 };
 
-// Scores `x` (log2 units, -inf where masked) of SUB blocks of 16 slots whose
-// value scale is 2^v -> weights as B fragments; updates m, l and rescales O.
+// Factor of the scores from those of the head and of the keys, both > 0.  Kept
+// where a masked -inf stays -inf and a dot product of 0 stays 0.
+__device__ __forceinline__ float score_factor(float q, float k) { return fminf(fmaxf(q * k, 1e-37f), 1e37f); }
+
+// Dot products `x` (-inf where masked) of SUB blocks of 16 slots, to be multiplied
+// by f0, f1 (> 0, finite; heads 2t, 2t + 1) for scores in log2 units, with the value
+// scale 2^v -> weights as B fragments; updates m, l and rescales O.
 template <int D, int SUB>
-__device__ __forceinline__ void softmax_step(State<D>& st, float (&x)[SUB][4], int v, uint32_t (&pb)[SUB][2]) {
+__device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB][4], float f0, float f1, int v,
+                                             uint32_t (&pb)[SUB][2]) {
   float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
@@ -198,7 +223,7 @@ __device__ __forceinline__ void softmax_step(State<D>& st, float (&x)[SUB][4], i
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
   }
   const float fv = (float)v, inv = q8::exp2_int(-v);
-  const float n0 = fmaxf(st.m[0], mx0 + fv), n1 = fmaxf(st.m[1], mx1 + fv);
+  const float n0 = fmaxf(st.m[0], fmaf(mx0, f0, fv)), n1 = fmaxf(st.m[1], fmaf(mx1, f1, fv));
   const float a0 = fast_exp2(st.m[0] - n0), a1 = fast_exp2(st.m[1] - n1);
   st.m[0] = n0;
   st.m[1] = n1;
@@ -206,8 +231,8 @@ __device__ __forceinline__ void softmax_step(State<D>& st, float (&x)[SUB][4], i
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
-    const float p0 = fast_exp2(x[u][0] + c0), p1 = fast_exp2(x[u][1] + c1);
-    const float p2 = fast_exp2(x[u][2] + c0), p3 = fast_exp2(x[u][3] + c1);
+    const float p0 = fast_exp2(fmaf(x[u][0], f0, c0)), p1 = fast_exp2(fmaf(x[u][1], f1, c1));
+    const float p2 = fast_exp2(fmaf(x[u][2], f0, c0)), p3 = fast_exp2(fmaf(x[u][3], f1, c1));
     s0 += p0 + p2;
     s1 += p1 + p3;
     pb[u][0] = movmatrix_trans(pack_f16x2(p0, p1));
@@ -228,17 +253,14 @@ __device__ __forceinline__ void softmax_step(State<D>& st, float (&x)[SUB][4], i
 
 }  // namespace
 
-// NT = number of 8-head n-tiles (ceil(G / 8)); NW = warps; SUB = 16-slot
-// blocks that a warp takes at a time; R = tiles (keys or values of a piece) in
-// a warp's ring.
-template <int D, int NT, int NW, int SUB, int R, int FMT>
-__global__ void __launch_bounds__(NW * 32)
+// NT = number of 8-head n-tiles (ceil(G / 8)); NW = warps; R = tiles (32 rows
+// of keys or of values) in a warp's ring.
+template <int D, int NT, int NW, int R, int FMT>
+__global__ void __launch_bounds__(NW * 32, 8 / NW)
 swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
   using F = Q8Frag<D>;
-  constexpr int kPiece = kSub * SUB;
-  constexpr int kTile = kPiece * D;
-  static_assert(kQ8Block % kPiece == 0, "a piece has one scale");
+  constexpr int kTile = kTileRows * D;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem_al = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024;
   float* smem = reinterpret_cast<float*>(smem_al);
@@ -249,10 +271,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   const int G = p.n_q_heads / p.n_kv_heads;
   const int W = p.window;
 
-  // each warp streams its own pieces: tiles K0 V0 K1 V1 ... through a ring of R,
-  // one barrier a place, filled by TMA and freed by the warp itself
+  // each warp streams its own blocks, K0 K1 V0 V1 of one after those of the other, through a
+  // ring of R tiles, one barrier a place, filled by TMA and freed by the warp itself
   const uint32_t ring = tc::smem_u32(smem_al) + warp * R * kTile;
-  const uint32_t bars = tc::smem_u32(smem_al) + q8_ring_bytes<D, NT, NW, SUB, R>() + 16 + warp * R * 8;
+  const uint32_t bars = tc::smem_u32(smem_al) + q8_ring_bytes<D, NT, NW, R>() + 16 + warp * R * 8;
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < R; ++i) tc::mbar_init(bars + 8 * i, 1);
@@ -264,6 +286,21 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
 
   wait_prior_grid();
   allow_next_grid();
+  const size_t unit = (size_t)b * p.n_kv_heads + kvh;
+  // Q is asked for before the ring's tiles, which would keep it waiting for as long as it takes to
+  // fill every ring (about 4 us).  Lane (g, t) holds head 8 nt + g.
+  uint32_t qf[NT][2 * F::kKWords];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int hl = nt * 8 + g;
+    const __nv_bfloat16* qrow = p.q + (unit * G + (hl < G ? hl : 0)) * D;
+#pragma unroll
+    for (int w = 0; w < F::kKWords; ++w) {
+      const uint2 x = hl < G ? ldg_stream8(qrow + key_elem<D>(t, w)) : make_uint2(0, 0);
+      qf[nt][2 * w] = x.x;
+      qf[nt][2 * w + 1] = x.y;
+    }
+  }
   const long long pos = p.pos[b];
   if (pos < 0) {   // every CTA of the sequence leaves here, whole clusters at a time
     if (threadIdx.x == 0) raise_status(p.status, SWA_ERR_DEVICE_ARG);
@@ -278,7 +315,6 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   const int r_end = r_stop < n_valid ? r_stop : n_valid;
   const bool owner = s_new >= r_begin && s_new < r_stop;
 
-  const size_t unit = (size_t)b * p.n_kv_heads + kvh;
   const int n_blocks = (W + kQ8Block - 1) / kQ8Block;
   const float* ksc = p.ring.k_scale + unit * n_blocks;
   const float* vsc = p.ring.v_scale + unit * n_blocks;
@@ -287,50 +323,63 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   const __nv_bfloat16* kn = p.k_new + unit * D;
   const __nv_bfloat16* vn = p.v_new + unit * D;
 
-  // rows [first_row(x), r_end) of the piece at slot x are held in 8 bits and in the window
-  auto first_row = [&](int x) { return (x >= blk0 && x <= s_new) ? s_new + 1 : x; };
-  auto next_piece = [&](int x) {
-    do x += NW * kPiece;
-    while (x < r_end && first_row(x) >= min(x + kPiece, r_end));
-    return x;
+  // The warp's blocks: those of its split in turn.  Rows [first_row(x), r_end) of the block at
+  // slot x are held in 8 bits and in the window; the block being filled may have none.
+  auto first_row = [&](int x) { return x == blk0 ? s_new + 1 : x; };
+  const int skip = s_new + 1 >= min(blk0 + kQ8Block, n_valid) ? blk0 : -1;
+  auto next_block = [&](int x) {
+    x += NW * kQ8Block;
+    return x == skip ? x + NW * kQ8Block : x;
   };
-  // the tile after the last one issued: piece, whether its values, place in the ring
-  int is_x = next_piece(r_begin + warp * kPiece - NW * kPiece), is_v = 0, is_at = 0;
+  // The block being filled, 16 rows to a warp: keys and values are the ring's first tiles (as large as
+  // 32 rows of bytes), rows before row_new from the tail, row_new from k_new / v_new.
+  const int y0 = warp * kSub;
+  const bool has_tail = owner && y0 <= row_new;
+  // the tile after the last one issued: its block, which of the block's, its place in the ring
+  int is_x = next_block(r_begin + (warp - NW) * kQ8Block), is_i = 0, is_at = 0;
   auto issue = [&]() {
     if (is_x >= r_end) return;
     if (lane == 0) {
       tc::mbar_arrive_expect_tx(bars + 8 * is_at, kTile);
-      tc::tma_load_3d(ring + is_at * kTile, is_v ? &v_map : &k_map, 0, is_x, (int)unit, bars + 8 * is_at);
+      tc::tma_load_3d(ring + is_at * kTile, is_i < kTiles ? &k_map : &v_map, 0,
+                      is_x + (is_i % kTiles) * kTileRows, (int)unit, bars + 8 * is_at);
     }
-    if (is_v) is_x = next_piece(is_x);
-    is_v ^= 1;
     is_at = is_at + 1 == R ? 0 : is_at + 1;
+    if (++is_i == 2 * kTiles) {
+      is_i = 0;
+      is_x = next_block(is_x);
+    }
   };
   int x0 = is_x;
+  if (has_tail) {
+    if (lane == 0) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) issue();
+      for (int i = 0; i < 2; ++i) {
+        const int old = row_new - y0 < kSub ? row_new - y0 : kSub;
+        const uint32_t row_bytes = 2 * D, dst = ring + i * kTile, bar = bars + 8 * i;
+        tc::mbar_arrive_expect_tx(bar, (old < kSub ? old + 1 : kSub) * row_bytes);
+        if (old > 0) tc::bulk_load(dst, (i == 0 ? kt : vt) + (size_t)y0 * D, old * row_bytes, bar);
+        if (old < kSub) tc::bulk_load(dst + old * row_bytes, i == 0 ? kn : vn, row_bytes, bar);
+      }
+    }
+    is_at = 2;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (i < R - 2 || !has_tail) issue();
   float ks = 0.f, vs = 1.f;
   if (x0 < r_end) {
     ks = ksc[x0 / kQ8Block];
     vs = vsc[x0 / kQ8Block];
   }
 
-  // Q as the B operand of S^T = K Q^T, f16: lane (g, t) holds head 8 nt + g.
-  uint32_t qf[NT][2 * F::kKWords];
+  // Q as the B operand of S^T = K Q^T, f16
   float qs[NT][2];                                   // factor of the scores of heads 2t, 2t + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int hl = nt * 8 + g;
-    const bool hv = hl < G;
-    const __nv_bfloat16* qrow = p.q + ((size_t)b * p.n_q_heads + (size_t)kvh * G + (hv ? hl : 0)) * D;
     uint32_t m = 0;
 #pragma unroll
-    for (int w = 0; w < F::kKWords; ++w) {
-      const uint2 x = hv ? ldg_stream8(qrow + key_elem<D>(t, w)) : make_uint2(0, 0);
-      qf[nt][2 * w] = x.x;
-      qf[nt][2 * w + 1] = x.y;
-      m = amax_word(amax_word(m, x.x), x.y);
-    }
+    for (int w = 0; w < 2 * F::kKWords; ++w) m = amax_word(m, qf[nt][w]);
     m = max(m & 0xffffu, m >> 16);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -352,154 +401,175 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     for (int mt = 0; mt < F::kMTiles; ++mt) st[nt].o[mt][0] = st[nt].o[mt][1] = st[nt].o[mt][2] = st[nt].o[mt][3] = 0.f;
   }
 
-  if (owner) {
-    // rows 0 .. row_new of the block being filled, 16 at a time: rows before
-    // row_new from the tail, row_new from k_new / v_new
-    for (int y0 = warp * kSub; y0 <= row_new; y0 += NW * kSub) {
-      uint32_t kw[2][2 * F::kKWords], vw[4][F::kMTiles];
-      uint32_t km = 0, vm = 0;
+  bool ok = true;
+  int at = 0, phase = 0;                       // place and phase of the next tile to read
+  // waits for the next tile (its address); once a wait has run out there is nothing more to wait for
+  auto take = [&]() -> uint32_t {
+    if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, phase, p.status));
+    return ring + at * kTile;
+  };
+  // every lane has read the tile: the next one goes into its place
+  auto done = [&]() {
+    __syncwarp();
+    if (ok) issue();
+    if (++at == R) at = 0, phase ^= 1;
+  };
+  if (has_tail) {
+    uint32_t tile = take();
+    uint32_t tk[2][2 * F::kKWords], tv[4][F::kMTiles];
+    uint32_t km = 0, vm = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = y0 + i * 8 + g;
-        const __nv_bfloat16* row = r == row_new ? kn : kt + (size_t)r * D;
+    for (int i = 0; i < 2; ++i) {
+      const int r = y0 + i * 8 + g;
 #pragma unroll
-        for (int w = 0; w < F::kKWords; ++w) {
-          const uint2 x = r <= row_new ? *reinterpret_cast<const uint2*>(row + key_elem<D>(t, w)) : make_uint2(0, 0);
-          kw[i][2 * w] = x.x;
-          kw[i][2 * w + 1] = x.y;
-          km = amax_word(amax_word(km, x.x), x.y);
-        }
+      for (int w = 0; w < F::kKWords; ++w) {
+        uint2 x = lds64(tile + (i * 8 + g) * (2 * D) + 2 * key_elem<D>(t, w));
+        if (r > row_new) x = make_uint2(0, 0);
+        tk[i][2 * w] = x.x;
+        tk[i][2 * w + 1] = x.y;
+        km = amax_word(amax_word(km, x.x), x.y);
       }
+    }
+    done();
+    tile = take();
+    if (ok) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = y0 + 2 * t + (i & 1) + (i >> 1) * 8;
-        const __nv_bfloat16* row = r == row_new ? vn : vt + (size_t)r * D;
+        const int ri = 2 * t + (i & 1) + (i >> 1) * 8, r = y0 + ri;
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt) {
-          vw[i][mt] = r <= row_new ? *reinterpret_cast<const uint32_t*>(row + g * (D / 8) + 2 * mt) : 0u;
-          vm = amax_word(vm, vw[i][mt]);
+          uint32_t x = lds32(tile + ri * (2 * D) + 2 * (g * (D / 8) + 2 * mt));
+          tv[i][mt] = r > row_new ? 0u : x;
+          vm = amax_word(vm, tv[i][mt]);
         }
       }
+      done();
       const int ke = f16_exp(__reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16)));
       const int ve = f16_exp(__reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16)));
-      const float kf = q8::exp2_int(-ke), vf = q8::exp2_int(-ve), ks = q8::exp2_int(ke);
+      const float kf = q8::exp2_int(-ke), vf = q8::exp2_int(-ve), ks16 = q8::exp2_int(ke);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int w = 0; w < 2 * F::kKWords; ++w) kw[i][w] = bf16_to_f16(kw[i][w], kf);
+        for (int w = 0; w < 2 * F::kKWords; ++w) tk[i][w] = bf16_to_f16(tk[i][w], kf);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int mt = 0; mt < F::kMTiles; ++mt) vw[i][mt] = bf16_to_f16(vw[i][mt], vf);
+        for (int mt = 0; mt < F::kMTiles; ++mt) tv[i][mt] = bf16_to_f16(tv[i][mt], vf);
       const bool ok0 = y0 + g <= row_new, ok1 = y0 + 8 + g <= row_new;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int w = 0; w < F::kKWords; ++w)
-          mma_f16(x[0], kw[0][2 * w], kw[1][2 * w], kw[0][2 * w + 1], kw[1][2 * w + 1], qf[nt][2 * w],
+          mma_f16(x[0], tk[0][2 * w], tk[1][2 * w], tk[0][2 * w + 1], tk[1][2 * w + 1], qf[nt][2 * w],
                   qf[nt][2 * w + 1]);
-        // the two powers of two one after the other: their product may leave fp32's range
-        x[0][0] = ok0 ? x[0][0] * ks * qs[nt][0] : -CUDART_INF_F;
-        x[0][1] = ok0 ? x[0][1] * ks * qs[nt][1] : -CUDART_INF_F;
-        x[0][2] = ok1 ? x[0][2] * ks * qs[nt][0] : -CUDART_INF_F;
-        x[0][3] = ok1 ? x[0][3] * ks * qs[nt][1] : -CUDART_INF_F;
+        if (!ok0) x[0][0] = x[0][1] = -CUDART_INF_F;
+        if (!ok1) x[0][2] = x[0][3] = -CUDART_INF_F;
         uint32_t pb[1][2];
-        softmax_step<D, 1>(st[nt], x, ve, pb);
+        softmax_step<D, 1>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), ve, pb);
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt)
-          mma_f16(st[nt].o[mt], prmt(vw[0][mt], vw[1][mt], 0x5410), prmt(vw[0][mt], vw[1][mt], 0x7632),
-                  prmt(vw[2][mt], vw[3][mt], 0x5410), prmt(vw[2][mt], vw[3][mt], 0x7632), pb[0][0], pb[0][1]);
+          mma_f16(st[nt].o[mt], prmt(tv[0][mt], tv[1][mt], 0x5410), prmt(tv[0][mt], tv[1][mt], 0x7632),
+                  prmt(tv[2][mt], tv[3][mt], 0x5410), prmt(tv[2][mt], tv[3][mt], 0x7632), pb[0][0], pb[0][1]);
       }
     }
   }
 
-  bool ok = true;
-  int at = 0, phase = 0;                       // place and phase of the next tile to read
-  while (x0 < r_end) {
-    const int lo = first_row(x0), hi = x0 + kPiece < r_end ? x0 + kPiece : r_end;
-    const int x1 = next_piece(x0);
-    float ks1 = 0.f, vs1 = 1.f;                // the next piece's scales, a piece ahead
+  while (ok && x0 < r_end) {
+    const int lo = first_row(x0), hi = x0 + kQ8Block < r_end ? x0 + kQ8Block : r_end;
+    const bool partial = lo > x0 || hi < x0 + kQ8Block;
+    const int x1 = next_block(x0);
+    float ks1 = 0.f, vs1 = 1.f;                // the next block's scales, a block ahead
     if (x1 < r_end) {
       ks1 = ksc[x1 / kQ8Block];
       vs1 = vsc[x1 / kQ8Block];
     }
-    const int ve = q8::exp_of(vs);
 
-    if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, phase, p.status)))) break;
-    uint32_t tile = ring + at * kTile;
-    float x[NT][SUB][4];
+    float x[NT][kSubs][4];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      uint32_t kw[2][F::kKWords];
+    for (int h = 0; h < kTiles; ++h) {
+      const uint32_t tile = take();
+      if (!ok) break;
+      // the tile goes to registers whole and its place is freed before the arithmetic: what a
+      // place holds while it waits to be read is not in flight
+      uint32_t kw[kTileSubs][2][F::kKWords];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) load_key8<D>(kw[i], tile, u * kSub + i * 8 + g, t);
+      for (int s = 0; s < kTileSubs; ++s)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt][u][0] = x[nt][u][1] = x[nt][u][2] = x[nt][u][3] = 0.f;
+        for (int i = 0; i < 2; ++i) load_key8<D>(kw[s][i], tile, s * kSub + i * 8 + g, t);
+      done();
 #pragma unroll
-      for (int w = 0; w < F::kKWords; ++w) {
-        uint32_t a0, a1, a2, a3;
-        q8::unpack4<FMT>(kw[0][w], a0, a2);
-        q8::unpack4<FMT>(kw[1][w], a1, a3);
+      for (int s = 0; s < kTileSubs; ++s) {
+        const int u = h * kTileSubs + s;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt][u], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+        for (int nt = 0; nt < NT; ++nt) x[nt][u][0] = x[nt][u][1] = x[nt][u][2] = x[nt][u][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < F::kKWords; ++w) {
+          uint32_t a0, a1, a2, a3;
+          q8::unpack4<FMT>(kw[s][0][w], a0, a2);
+          q8::unpack4<FMT>(kw[s][1][w], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt][u], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+        }
       }
     }
-    __syncwarp();
-    issue();                                   // into the place of the keys just read
-    if (++at == R) at = 0, phase ^= 1;
+    if (!ok) break;
 
-    const bool partial = lo > x0 || hi < x0 + kPiece;
-    uint32_t pb[NT][SUB][2];
+    uint32_t pb[NT][kSubs][2];
+    if (partial) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float f0 = qs[nt][0] * ks, f1 = qs[nt][1] * ks;
+      for (int u = 0; u < kSubs; ++u) {
+        const int r0 = x0 + u * kSub + g, r1 = r0 + 8;
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        x[nt][u][0] *= f0;
-        x[nt][u][1] *= f1;
-        x[nt][u][2] *= f0;
-        x[nt][u][3] *= f1;
-      }
-      if (partial) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          const int r0 = x0 + u * kSub + g, r1 = r0 + 8;
+        for (int nt = 0; nt < NT; ++nt) {
           if (r0 < lo || r0 >= hi) x[nt][u][0] = x[nt][u][1] = -CUDART_INF_F;
           if (r1 < lo || r1 >= hi) x[nt][u][2] = x[nt][u][3] = -CUDART_INF_F;
         }
       }
-      softmax_step<D, SUB>(st[nt], x[nt], ve, pb[nt]);
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      softmax_step<D, kSubs>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks), q8::exp_of(vs),
+                             pb[nt]);
 
-    if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, phase, p.status)))) break;
-    tile = ring + at * kTile;
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      uint32_t vw[4][F::kVWords];
+    for (int h = 0; h < kTiles; ++h) {
+      const uint32_t tile = take();
+      if (!ok) break;
+      uint32_t vw[kTileSubs][4][F::kVWords];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = u * kSub + 2 * t + (i & 1) + (i >> 1) * 8;
-        load_val8<D>(vw[i], tile, r, g);
-        if (partial && (x0 + r < lo || x0 + r >= hi)) {   // 0 times what the row holds must be 0
+      for (int s = 0; s < kTileSubs; ++s) {
 #pragma unroll
-          for (int w = 0; w < F::kVWords; ++w) vw[i][w] = 0;
+        for (int i = 0; i < 4; ++i) load_val8<D>(vw[s][i], tile, s * kSub + 2 * t + (i & 1) + (i >> 1) * 8, g);
+      }
+      done();
+      if (partial) {                           // 0 times what a masked row holds must be 0
+#pragma unroll
+        for (int s = 0; s < kTileSubs; ++s) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int slot = x0 + h * kTileRows + s * kSub + 2 * t + (i & 1) + (i >> 1) * 8;
+#pragma unroll
+            for (int w = 0; w < F::kVWords; ++w) vw[s][i][w] = slot < lo || slot >= hi ? 0u : vw[s][i][w];
+          }
         }
       }
 #pragma unroll
-      for (int mt = 0; mt < F::kMTiles; ++mt) {
-        // bytes 2 mt, 2 mt + 1 of rows (2t, 2t + 1) and (2t + 8, 2t + 9), paired by element
-        const uint32_t sel = (mt & 1) ? 0x7362 : 0x5140;
-        uint32_t a0, a1, a2, a3;
-        q8::unpack4<FMT>(prmt(vw[0][mt / 2], vw[1][mt / 2], sel), a0, a1);
-        q8::unpack4<FMT>(prmt(vw[2][mt / 2], vw[3][mt / 2], sel), a2, a3);
+      for (int s = 0; s < kTileSubs; ++s) {
+        const int u = h * kTileSubs + s;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(st[nt].o[mt], a0, a1, a2, a3, pb[nt][u][0], pb[nt][u][1]);
+        for (int mt = 0; mt < F::kMTiles; ++mt) {
+          // bytes 2 mt, 2 mt + 1 of rows (2t, 2t + 1) and (2t + 8, 2t + 9), paired by element
+          const uint32_t sel = (mt & 1) ? 0x7362 : 0x5140;
+          uint32_t a0, a1, a2, a3;
+          q8::unpack4<FMT>(prmt(vw[s][0][mt / 2], vw[s][1][mt / 2], sel), a0, a1);
+          q8::unpack4<FMT>(prmt(vw[s][2][mt / 2], vw[s][3][mt / 2], sel), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(st[nt].o[mt], a0, a1, a2, a3, pb[nt][u][0], pb[nt][u][1]);
+        }
       }
     }
-    __syncwarp();
-    issue();
-    if (++at == R) at = 0, phase ^= 1;
+    if (!ok) break;
     x0 = x1;
     ks = ks1;
     vs = vs1;
@@ -513,18 +583,17 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
 
   // ---- merge the NW warps of the CTA ----
-  // smem (the rings, once every warp is done with its own): m[NW][G8], l[NW][G8], O[NW][G8][kOS], then
-  // the CTA's m[G8], l[G8], O[G8][D]
+  // in the rings, once every warp is done with its own: m[NW][G8], l[NW][G8], O[NW][G8][kOS]
   __syncthreads();
   constexpr int G8 = 8 * NT;
   constexpr int kOS = q8_o_stride<D>();
   float* sm_m = smem;
   float* sm_l = sm_m + NW * G8;
   float* sm_o = sm_l + NW * G8;
-  float* cta_m = sm_o + (size_t)NW * G8 * kOS;
-  float* cta_l = cta_m + G8;
-  float* cta_o = cta_l + G8;
-  uint32_t* red = reinterpret_cast<uint32_t*>(smem_al + q8_ring_bytes<D, NT, NW, SUB, R>());
+  uint32_t* red = reinterpret_cast<uint32_t*>(smem_al + q8_ring_bytes<D, NT, NW, R>());
+  // what the peers of a cluster send: (m, l)[rank][G8] and O[rank][share]
+  float* peer_ml = reinterpret_cast<float*>(smem_al + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8);
+  float* peer_o = peer_ml + kMaxCluster * G8 * 2;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float l0 = st[nt].l[0], l1 = st[nt].l[1];
@@ -553,6 +622,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   __syncthreads();
 
   const int hq0 = kvh * G;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cl = cg::this_cluster();
+  const int n_cl = p.cluster ? p.n_splits : 1, rank = p.cluster ? split : 0;
+  const int per = (G * D + n_cl - 1) / n_cl;         // outputs that a CTA of the cluster merges
   for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
     const int h = idx / D, dd = idx % D;
     float M = -CUDART_INF_F;
@@ -571,11 +644,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     if (p.n_splits == 1) {
       store_out(p.out, bh * D + dd, O / L, p.out_f32);
     } else if (p.cluster) {
-      cta_o[h * D + dd] = O;
-      if (dd == 0) {
-        cta_m[h] = M;
-        cta_l[h] = L;
-      }
+      // each output to the CTA that merges it, m and l to all
+      cl.map_shared_rank(peer_o, idx / per)[rank * per + idx % per] = O;
+      if (dd < n_cl)
+        reinterpret_cast<float2*>(cl.map_shared_rank(peer_ml, dd))[rank * G8 + h] = make_float2(M, L);
     } else {
       p.ws_o[(bh * p.n_splits + split) * D + dd] = O;
       if (dd == 0) {
@@ -586,38 +658,20 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
 
   if (p.cluster) {
-    // each CTA of the pair's cluster merges a share of the G x d outputs
-    namespace cg = cooperative_groups;
-    cg::cluster_group cl = cg::this_cluster();
-    cl.sync();
-    const int R = p.n_splits;
-    const int per = (G * D + R - 1) / R, begin = (int)cl.block_rank() * per;
-    for (int idx = begin + threadIdx.x; idx < begin + per && idx < G * D; idx += NW * 32) {
+    cl.sync();   // all has been sent; every CTA of the pair's cluster comes here
+    for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < G * D; idx += NW * 32) {
       const int h = idx / D;
-      float m_r[kMaxCluster], l_r[kMaxCluster], o_r[kMaxCluster];
       float M = -CUDART_INF_F;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        m_r[r] = -CUDART_INF_F;
-        l_r[r] = o_r[r] = 0.f;
-        if (r < R) {
-          m_r[r] = cl.map_shared_rank(cta_m, r)[h];
-          l_r[r] = cl.map_shared_rank(cta_l, r)[h];
-          o_r[r] = cl.map_shared_rank(cta_o, r)[idx];
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) M = fmaxf(M, m_r[r]);
+      for (int r = 0; r < n_cl; ++r) M = fmaxf(M, reinterpret_cast<float2*>(peer_ml)[r * G8 + h].x);
       float L = 0.f, O = 0.f;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        const float sc = m_r[r] == -CUDART_INF_F ? 0.f : fast_exp2(m_r[r] - M);
-        L += sc * l_r[r];
-        O += sc * o_r[r];
+      for (int r = 0; r < n_cl; ++r) {
+        const float2 ml = reinterpret_cast<float2*>(peer_ml)[r * G8 + h];
+        const float sc = ml.x == -CUDART_INF_F ? 0.f : fast_exp2(ml.x - M);
+        L += sc * ml.y;
+        O += sc * peer_o[r * per + idx - rank * per];
       }
       store_out(p.out, ((size_t)b * p.n_q_heads + hq0) * D + idx, O / L, p.out_f32);
     }
-    cl.sync();  // this CTA's partial stays until every peer has read it
   }
 
   if (owner) {
@@ -666,10 +720,10 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-template <int D, int NT, int NW, int SUB, int R, int FMT>
+template <int D, int NT, int NW, int R, int FMT>
 cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
-  constexpr int smem = q8_smem_bytes<D, NT, NW, SUB, R>();
-  auto kern = swa_q8_decode_kernel<D, NT, NW, SUB, R, FMT>;
+  constexpr int smem = q8_smem_bytes<D, NT, NW, R>();
+  auto kern = swa_q8_decode_kernel<D, NT, NW, R, FMT>;
   if (smem > 48 * 1024) {
     // raised once per device (the attribute persists for the process)
     static bool set[kMaxDevices] = {};
@@ -708,23 +762,15 @@ cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStre
   return cudaLaunchKernelEx(&ccfg, swa_q8_decode_combine_kernel<D>, p);
 }
 
-#ifndef Q8_SUB
-#define Q8_SUB 2
-#endif
-#ifndef Q8_R4
-#define Q8_R4 3
-#endif
-#ifndef Q8_R8
-#define Q8_R8 3
-#endif
+// 8 warps an SM, with 24 KB of tiles in flight for each.
+constexpr int kRing = 6;
+
 template <int D, int FMT>
 cudaError_t launch_f(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
   const bool wide = p.n_q_heads / p.n_kv_heads > 8;
   if (p.warps == 8)
-    return wide ? launch_t<D, 2, 8, Q8_SUB, Q8_R8, FMT>(p, maps, stream)
-                : launch_t<D, 1, 8, Q8_SUB, Q8_R8, FMT>(p, maps, stream);
-  return wide ? launch_t<D, 2, 4, Q8_SUB, Q8_R4, FMT>(p, maps, stream)
-              : launch_t<D, 1, 4, Q8_SUB, Q8_R4, FMT>(p, maps, stream);
+    return wide ? launch_t<D, 2, 8, kRing, FMT>(p, maps, stream) : launch_t<D, 1, 8, kRing, FMT>(p, maps, stream);
+  return wide ? launch_t<D, 2, 4, kRing, FMT>(p, maps, stream) : launch_t<D, 1, 4, kRing, FMT>(p, maps, stream);
 }
 
 template <int D>
@@ -741,25 +787,19 @@ Q8DecodeSplit q8_decode_split(int batch, int n_q_heads, int n_kv_heads, int wind
   const long long units = (long long)batch * n_kv_heads;
   Q8DecodeSplit s;
   const long long n_blocks = ((long long)window + kQ8Block - 1) / kQ8Block;
-  long long splits;
-  if (units < 148) {
-    splits = 148 / units;
-    if (splits > kMaxCluster) splits = kMaxCluster;
-    s.warps = 8;
-  } else {
-    splits = 148 * 4 / units;
-    s.warps = 4;
-  }
-  if (splits < 1) splits = 1;
+  long long splits = 1;
+  if (units < 148) splits = 148 / units;
+  s.warps = units < 148 ? 8 : 4;
+  if (splits > kMaxCluster) splits = kMaxCluster;
   if (splits > n_blocks) splits = n_blocks;
   const long long per = (n_blocks + splits - 1) / splits;
   s.slots_per_split = (int)(per * kQ8Block);
   s.n_splits = (int)((n_blocks + per - 1) / per);
-  s.cluster = (units < 148 && s.n_splits > 1) ? 1 : 0;
+  s.cluster = s.n_splits > 1 ? 1 : 0;
   return s;
 }
 
-int q8_decode_box_rows() { return Q8_SUB * kSub; }
+int q8_decode_box_rows() { return kTileRows; }
 
 cudaError_t launch_q8_decode(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
   switch (p.head_dim) {
