@@ -41,8 +41,8 @@ rotary positions of q and k::
 from __future__ import annotations
 
 import ctypes
-import contextlib
 import dataclasses
+import functools
 import math
 import os
 import threading
@@ -117,6 +117,10 @@ class Dims:
     def c(self) -> _CDims:
         return _CDims(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.window,
                       float(self.scale), _DTYPES[self.out_dtype])
+
+    @functools.cached_property
+    def _ref(self):
+        return ctypes.byref(self.c())
 
     @property
     def torch_out_dtype(self) -> torch.dtype:
@@ -306,17 +310,10 @@ _Q8_DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 
 def _arg(name: str, t: torch.Tensor, shape, dtype: torch.dtype, dev: int) -> int:
     """Address of a dense tensor of this shape, type and device; ValueError for another."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
-                         + ("" if t.is_contiguous() else ", not contiguous"))
-    return t.data_ptr()
-
-
-def _workspace(t: torch.Tensor, dev: int):
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}, got one on {t.device}")
-    return t.data_ptr(), t.numel() * t.element_size()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
 
 
 def _device_of(name: str, t: torch.Tensor) -> int:
@@ -325,17 +322,26 @@ def _device_of(name: str, t: torch.Tensor) -> int:
     return t.get_device()
 
 
-def _on(dev: int):
-    """Makes `dev` the current device for a call (nothing where it already is)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _stream_on(stream, dev: int) -> ctypes.c_void_p:
+def _run(dev: int, stream, name: str, *args) -> None:
+    """The library's call `name` with dev current (where the tensors are), on `stream` or dev's current one."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
-        raise ValueError(f"stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
-    return _stream(stream)
+        stream = _current_stream(dev)
+    else:
+        if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+            raise ValueError(f"stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
+        stream = _stream(stream)
+    fn = getattr(_lib or load_library(), name)
+    if _current_device() == dev:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != SWA_OK:
+        _check(rc)
 
 
 @dataclasses.dataclass(frozen=True, eq=False)
@@ -367,7 +373,7 @@ class CacheQ8:
                 _arg("v_scale", self.v_scale, blocks, torch.float32, dev),
                 _arg("k_tail", self.k_tail, tail, torch.bfloat16, dev),
                 _arg("v_tail", self.v_tail, tail, torch.bfloat16, dev)]
-        object.__setattr__(self, "_c", _CCacheQ8(*ptrs, _Q8_FORMATS[self.k.dtype]))
+        object.__setattr__(self, "_ref", ctypes.byref(_CCacheQ8(*ptrs, _Q8_FORMATS[self.k.dtype])))
         object.__setattr__(self, "_dev", dev)
         object.__setattr__(self, "_shape", (B, H, W, d))
 
@@ -398,17 +404,15 @@ def cache_append_q8(dims: Dims, cache: CacheQ8, k, v, start_pos, n_tokens, strea
     """swa_q8_append: k/v [B, T, Hkv, d] bf16 into the 8-bit cache, blocks that they fill up
     rounded, the rest in the tail."""
     dev = cache._for(dims)
-    B, T = dims.batch, int(k.shape[1])
+    B, T = dims.batch, k.shape[1]
     rows = (B, T, dims.n_kv_heads, dims.head_dim)
-    args = (_arg("k", k, rows, torch.bfloat16, dev), _arg("v", v, rows, torch.bfloat16, dev), T,
-            _arg("start_pos", start_pos, (B,), torch.int32, dev), _arg("n_tokens", n_tokens, (B,), torch.int32, dev))
-    with _on(dev):
-        _check(load_library().swa_q8_append(ctypes.byref(dims.c()), ctypes.byref(cache._c), *args,
-                                            _stream_on(stream, dev)))
+    _run(dev, stream, "swa_q8_append", dims._ref, cache._ref, _arg("k", k, rows, torch.bfloat16, dev),
+         _arg("v", v, rows, torch.bfloat16, dev), T, _arg("start_pos", start_pos, (B,), torch.int32, dev),
+         _arg("n_tokens", n_tokens, (B,), torch.int32, dev))
 
 
 def prefill_workspace_size_q8(dims: Dims, max_tokens: int) -> int:
-    return int(load_library().swa_q8_prefill_workspace_size(ctypes.byref(dims.c()), int(max_tokens)))
+    return int(load_library().swa_q8_prefill_workspace_size(dims._ref, int(max_tokens)))
 
 
 def prefill_workspace_q8(dims: Dims, max_tokens: int, device="cuda") -> torch.Tensor:
@@ -420,19 +424,17 @@ def prefill_chunk_q8(dims: Dims, out, q, k, v, cache: CacheQ8, start_pos, n_toke
                      stream=None) -> None:
     """swa_q8_prefill_chunk: out [B, T, Hq, d] = attention of chunk q over (8-bit cache + chunk k/v)."""
     dev = cache._for(dims)
-    B, T = dims.batch, int(q.shape[1])
+    B, T = dims.batch, q.shape[1]
     heads, rows = (B, T, dims.n_q_heads, dims.head_dim), (B, T, dims.n_kv_heads, dims.head_dim)
-    args = (_arg("out", out, heads, dims.torch_out_dtype, dev), _arg("q", q, heads, torch.bfloat16, dev),
-            _arg("k", k, rows, torch.bfloat16, dev), _arg("v", v, rows, torch.bfloat16, dev), T,
-            ctypes.byref(cache._c),
-            _arg("start_pos", start_pos, (B,), torch.int32, dev), _arg("n_tokens", n_tokens, (B,), torch.int32, dev),
-            *_workspace(workspace, dev))
-    with _on(dev):
-        _check(load_library().swa_q8_prefill_chunk(ctypes.byref(dims.c()), *args, _stream_on(stream, dev)))
+    _run(dev, stream, "swa_q8_prefill_chunk", dims._ref, _arg("out", out, heads, dims.torch_out_dtype, dev),
+         _arg("q", q, heads, torch.bfloat16, dev), _arg("k", k, rows, torch.bfloat16, dev),
+         _arg("v", v, rows, torch.bfloat16, dev), T, cache._ref, _arg("start_pos", start_pos, (B,), torch.int32, dev),
+         _arg("n_tokens", n_tokens, (B,), torch.int32, dev),
+         _arg("workspace", workspace, workspace.shape, workspace.dtype, dev), workspace.nbytes)
 
 
 def decode_workspace_size_q8(dims: Dims) -> int:
-    return int(load_library().swa_q8_decode_workspace_size(ctypes.byref(dims.c())))
+    return int(load_library().swa_q8_decode_workspace_size(dims._ref))
 
 
 def decode_workspace_q8(dims: Dims, device="cuda") -> torch.Tensor:
@@ -445,11 +447,10 @@ def decode_q8(dims: Dims, out, q, k_new, v_new, cache: CacheQ8, pos, workspace, 
     dev = cache._for(dims)
     B, d = dims.batch, dims.head_dim
     heads, rows = (B, dims.n_q_heads, d), (B, dims.n_kv_heads, d)
-    args = (_arg("out", out, heads, dims.torch_out_dtype, dev), _arg("q", q, heads, torch.bfloat16, dev),
-            _arg("k_new", k_new, rows, torch.bfloat16, dev), _arg("v_new", v_new, rows, torch.bfloat16, dev),
-            ctypes.byref(cache._c), _arg("pos", pos, (B,), torch.int32, dev), *_workspace(workspace, dev))
-    with _on(dev):
-        _check(load_library().swa_q8_decode(ctypes.byref(dims.c()), *args, _stream_on(stream, dev)))
+    _run(dev, stream, "swa_q8_decode", dims._ref, _arg("out", out, heads, dims.torch_out_dtype, dev),
+         _arg("q", q, heads, torch.bfloat16, dev), _arg("k_new", k_new, rows, torch.bfloat16, dev),
+         _arg("v_new", v_new, rows, torch.bfloat16, dev), cache._ref, _arg("pos", pos, (B,), torch.int32, dev),
+         _arg("workspace", workspace, workspace.shape, workspace.dtype, dev), workspace.nbytes)
 
 
 @dataclasses.dataclass(frozen=True, eq=False)
@@ -466,7 +467,7 @@ class Rope:
         dev = _device_of("inv_freq", self.inv_freq)
         n = self.inv_freq.numel()
         ptr = _arg("inv_freq", self.inv_freq, (n,), torch.float32, dev)
-        object.__setattr__(self, "_c", _CRope(ptr, 2 * n, int(self.interleaved), float(self.factor)))
+        object.__setattr__(self, "_ref", ctypes.byref(_CRope(ptr, 2 * n, int(self.interleaved), float(self.factor))))
         object.__setattr__(self, "_dev", dev)
 
 
@@ -503,14 +504,15 @@ def new_rope(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, 
 def _rows(name: str, t: torch.Tensor, shape, dev: int):
     """(address, elements from row to row) of q or k [B, T, H, d], heads dense, rows evenly spaced."""
     B, T, H, d = shape
-    s = t.stride()
-    ok = t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev
-    ok = ok and s[3] == 1 and (H == 1 or s[2] == d)
-    row = s[1] if T > 1 else s[0] if B > 1 else H * d
-    if not (ok and (B == 1 or s[0] == T * row)):
-        raise ValueError(f"{name}: expected a bfloat16 tensor of shape {tuple(shape)} on cuda:{dev} with dense heads and "
-                         f"evenly spaced rows, got {t.dtype} {tuple(t.shape)} with strides {s} on {t.device}")
-    return t.data_ptr(), row
+    if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), H * d
+        s = t.stride()
+        row = s[1] if T > 1 else s[0] if B > 1 else H * d
+        if s[3] == 1 and (H == 1 or s[2] == d) and (B == 1 or s[0] == T * row):
+            return t.data_ptr(), row
+    raise ValueError(f"{name}: expected a bfloat16 tensor of shape {tuple(shape)} on cuda:{dev} with dense heads and "
+                     f"evenly spaced rows, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def rope(dims: Dims, spec: Rope, q_out, k_out, q, k, start_pos, n_tokens=None, transpose: bool = False,
@@ -519,19 +521,16 @@ def rope(dims: Dims, spec: Rope, q_out, k_out, q, k, start_pos, n_tokens=None, t
     taken as they lie) turned to positions start_pos[b] + t, into dense q_out and k_out (which may be
     q and k if those are dense).  k and k_out may be None.  ``n_tokens`` None: all T rows.
     ``transpose`` gives the gradient for q and k from that for q_out and k_out."""
-    dev = _device_of("q", q)
-    if q.dim() != 4 or spec._dev != dev:
-        raise ValueError(f"q: expected [B, T, Hq, d] on cuda:{spec._dev}, got {tuple(q.shape)} on {q.device}")
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out: both or neither")
-    B, T, d = dims.batch, int(q.shape[1]), dims.head_dim
+    dev = spec._dev
+    B, T, d = dims.batch, q.shape[1], dims.head_dim
     heads, rows = (B, T, dims.n_q_heads, d), (B, T, dims.n_kv_heads, d)
     qp, qs = _rows("q", q, heads, dev)
-    kp, ks = _rows("k", k, rows, dev) if k is not None else (None, 0)
-    outs = (_arg("q_out", q_out, heads, torch.bfloat16, dev),
-            _arg("k_out", k_out, rows, torch.bfloat16, dev) if k is not None else None)
-    start = _arg("start_pos", start_pos, (B,), torch.int32, dev)
-    count = _arg("n_tokens", n_tokens, (B,), torch.int32, dev) if n_tokens is not None else None
-    with _on(dev):
-        _check(load_library().swa_rope(ctypes.byref(dims.c()), ctypes.byref(spec._c), *outs, qp, kp, qs, ks, T, start,
-                                       count, int(transpose), _stream_on(stream, dev)))
+    qo, kp, ks, ko = _arg("q_out", q_out, heads, torch.bfloat16, dev), None, 0, None
+    if k is not None or k_out is not None:
+        if k is None or k_out is None:
+            raise ValueError("k and k_out: both or neither")
+        kp, ks = _rows("k", k, rows, dev)
+        ko = _arg("k_out", k_out, rows, torch.bfloat16, dev)
+    _run(dev, stream, "swa_rope", dims._ref, spec._ref, qo, ko, qp, kp, qs, ks, T,
+         _arg("start_pos", start_pos, (B,), torch.int32, dev),
+         None if n_tokens is None else _arg("n_tokens", n_tokens, (B,), torch.int32, dev), 1 if transpose else 0)
