@@ -165,6 +165,8 @@ struct Q8DecodeParams {
   float* ws_o;                  // [B][Hq][n_splits][d] partial O (two launches)
   float* ws_ml;                 // [B][Hq][n_splits][2] partial (max, sum)
   int* status;
+  const int32_t* n_tokens;      // device [B], or NULL: one token, which is taken in
+  int max_tokens, groups;       // rows of a chunk, CTAs that share its columns
   int batch, n_q_heads, n_kv_heads, head_dim, window;
   int n_splits, slots_per_split;
   int warps;                    // warps per CTA
@@ -176,7 +178,11 @@ struct Q8DecodeParams {
 struct Q8DecodeSplit {
   int n_splits, slots_per_split, warps, cluster;
 };
-Q8DecodeSplit q8_decode_split(int batch, int n_q_heads, int n_kv_heads, int window, int head_dim);
+Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int groups);
+// Chunks of at most this many columns (rows x query heads of a kv head) go through launch_q8_decode
+// too, with q, k, v and out as in the prefill and start positions as pos.
+int q8_few_columns();
+int q8_chunk_groups(int columns);
 // TMA descriptors of the ring's keys and values: [B * Hkv][W][d] bytes, boxes of
 // q8_decode_box_rows() rows, swizzled by the row's size.
 struct Q8DecodeMaps {

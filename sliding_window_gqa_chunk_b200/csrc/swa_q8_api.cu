@@ -65,6 +65,38 @@ size_t ring_bytes(const swa_dims* dims) {   // of the keys or of the values
   return (size_t)dims->batch * dims->n_kv_heads * dims->window * dims->head_dim * sizeof(__nv_bfloat16);
 }
 
+// Fills in what decode steps and short chunks share, and launches.
+int launch_over_ring(swa::Q8DecodeParams& p, const swa_dims* dims, const swa_q8_cache* cache, void* out, const void* q,
+                     const void* k, const void* v, const int32_t* pos, const swa::Q8DecodeSplit& sp, void* stream,
+                     const char* what) {
+  p.out = out;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_new = static_cast<const __nv_bfloat16*>(k);
+  p.v_new = static_cast<const __nv_bfloat16*>(v);
+  p.pos = pos;
+  p.batch = dims->batch;
+  p.n_q_heads = dims->n_q_heads;
+  p.n_kv_heads = dims->n_kv_heads;
+  p.head_dim = dims->head_dim;
+  p.window = dims->window;
+  p.n_splits = sp.n_splits;
+  p.slots_per_split = sp.slots_per_split;
+  p.warps = sp.warps;
+  p.cluster = sp.cluster;
+  p.scale_log2 = dims->scale * 1.4426950408889634f;
+  p.out_f32 = dims->out_dtype == SWA_DTYPE_F32;
+  int rc = swa::api_status_word(&p.status);
+  if (rc) return rc;
+  swa::Q8DecodeMaps maps;
+  const long long pairs = (long long)dims->batch * dims->n_kv_heads;
+  const int box = swa::q8_decode_box_rows();
+  if ((rc = swa::api_encode_bytes(&maps.k, cache->k, dims->head_dim, dims->window, pairs, box, "cache k"))) return rc;
+  if ((rc = swa::api_encode_bytes(&maps.v, cache->v, dims->head_dim, dims->window, pairs, box, "cache v"))) return rc;
+  const cudaError_t e = swa::launch_q8_decode(p, maps, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return swa::api_ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -114,6 +146,18 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
   if (workspace_bytes < need)
     return swa::api_fail(SWA_ERR_WORKSPACE_TOO_SMALL, "q8 prefill workspace of %zu bytes, %zu needed",
                          workspace_bytes, need);
+  const int columns_per_row = dims->n_q_heads / dims->n_kv_heads;
+  if ((long long)max_tokens * columns_per_row <= swa::q8_few_columns()) {
+    // a few rows: straight over the ring's bytes
+    swa::Q8DecodeParams d;
+    d.ring = p.ring;
+    d.ws_o = d.ws_ml = nullptr;
+    d.n_tokens = n_tokens;
+    d.max_tokens = max_tokens;
+    d.groups = swa::q8_chunk_groups(max_tokens * columns_per_row);
+    const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, d.groups);
+    return launch_over_ring(d, dims, cache, out, q, k, v, start_pos, sp, stream, "swa_q8_prefill_chunk");
+  }
   // the prefill's own limit, before the ring is expanded: a refused call enqueues nothing
   const int hpc = swa::prefill_heads_per_cta(dims->n_q_heads, dims->n_kv_heads);
   const long long n_units =
@@ -138,8 +182,7 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
 
 size_t swa_q8_decode_workspace_size(const swa_dims* dims) {
   if (check_q8_dims(dims) != SWA_OK) return 0;
-  const swa::Q8DecodeSplit sp =
-      swa::q8_decode_split(dims->batch, dims->n_q_heads, dims->n_kv_heads, dims->window, dims->head_dim);
+  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1);
   if (sp.n_splits == 1 || sp.cluster) return 16;  // nothing needed; a non-zero size keeps callers simple
   return (size_t)dims->batch * dims->n_q_heads * sp.n_splits * (dims->head_dim + 2) * sizeof(float);
 }
@@ -158,36 +201,13 @@ int swa_q8_decode(const swa_dims* dims, void* out, const void* q, const void* k_
   if (workspace_bytes < need)
     return swa::api_fail(SWA_ERR_WORKSPACE_TOO_SMALL, "q8 decode workspace of %zu bytes, %zu needed",
                          workspace_bytes, need);
-  if ((rc = swa::api_status_word(&p.status))) return rc;
-  const swa::Q8DecodeSplit sp =
-      swa::q8_decode_split(dims->batch, dims->n_q_heads, dims->n_kv_heads, dims->window, dims->head_dim);
-  p.out = out;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
-  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
-  p.pos = pos;
-  const size_t bh = (size_t)dims->batch * dims->n_q_heads * sp.n_splits;
+  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1);
   p.ws_o = static_cast<float*>(workspace);
-  p.ws_ml = static_cast<float*>(workspace) + bh * dims->head_dim;
-  p.batch = dims->batch;
-  p.n_q_heads = dims->n_q_heads;
-  p.n_kv_heads = dims->n_kv_heads;
-  p.head_dim = dims->head_dim;
-  p.window = dims->window;
-  p.n_splits = sp.n_splits;
-  p.slots_per_split = sp.slots_per_split;
-  p.warps = sp.warps;
-  p.cluster = sp.cluster;
-  p.scale_log2 = dims->scale * 1.4426950408889634f;
-  p.out_f32 = dims->out_dtype == SWA_DTYPE_F32;
-  swa::Q8DecodeMaps maps;
-  const long long pairs = (long long)dims->batch * dims->n_kv_heads;
-  const int box = swa::q8_decode_box_rows();
-  if ((rc = swa::api_encode_bytes(&maps.k, cache->k, dims->head_dim, dims->window, pairs, box, "cache k"))) return rc;
-  if ((rc = swa::api_encode_bytes(&maps.v, cache->v, dims->head_dim, dims->window, pairs, box, "cache v"))) return rc;
-  const cudaError_t e = swa::launch_q8_decode(p, maps, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "swa_q8_decode");
-  return swa::api_ok();
+  p.ws_ml = p.ws_o + (size_t)dims->batch * dims->n_q_heads * sp.n_splits * dims->head_dim;
+  p.n_tokens = nullptr;
+  p.max_tokens = 1;
+  p.groups = 1;
+  return launch_over_ring(p, dims, cache, out, q, k_new, v_new, pos, sp, stream, "swa_q8_decode");
 }
 
 int swa_rope(const swa_dims* dims, const swa_rope_spec* spec, void* q_out, void* k_out, const void* q, const void* k,

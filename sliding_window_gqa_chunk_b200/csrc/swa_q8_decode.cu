@@ -45,6 +45,9 @@
 
 namespace swa {
 
+#ifndef Q8_FEW
+#define Q8_FEW 128
+#endif
 namespace {
 
 constexpr int kSub = 16;            // slots of one mma block
@@ -53,6 +56,7 @@ constexpr int kTileRows = 32;       // rows of a TMA tile
 constexpr int kTileSubs = kTileRows / kSub;
 constexpr int kTiles = kQ8Block / kTileRows;  // tiles of a block's keys (and of its values)
 constexpr int kMaxCluster = 8;      // portable cluster size
+constexpr int kChunkRows = 128;     // rows of the longest chunk that comes here
 
 // Row fragments of a lane: bytes of a key row (D / 4) and of a value row (D / 8).
 template <int D>
@@ -187,6 +191,10 @@ constexpr int q8_smem_bytes() {
   return 1024 + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8 + 4 * q8_peer_floats<D, NT>();
 }
 
+// A CTA's shared memory may be written by its peers once it has begun: no memory is ordered by this.
+__device__ __forceinline__ void cluster_begun_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
+__device__ __forceinline__ void cluster_begun_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void store_out(void* out, size_t i, float x, int f32) {
   if (f32) reinterpret_cast<float*>(out)[i] = x;
   else reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
@@ -208,7 +216,8 @@ __device__ __forceinline__ float score_factor(float q, float k) { return fminf(f
 // Dot products `x` (-inf where masked) of SUB blocks of 16 slots, to be multiplied
 // by f0, f1 (> 0, finite; heads 2t, 2t + 1) for scores in log2 units, with the value
 // scale 2^v -> weights as B fragments; updates m, l and rescales O.
-template <int D, int SUB>
+// GUARD: a column may have no unmasked row (else every one has).
+template <int D, int SUB, bool GUARD>
 __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB][4], float f0, float f1, int v,
                                              uint32_t (&pb)[SUB][2]) {
   float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
@@ -224,10 +233,12 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
   }
   const float fv = (float)v, inv = q8::exp2_int(-v);
   const float n0 = fmaxf(st.m[0], fmaf(mx0, f0, fv)), n1 = fmaxf(st.m[1], fmaf(mx1, f1, fv));
-  const float a0 = fast_exp2(st.m[0] - n0), a1 = fast_exp2(st.m[1] - n1);
+  // where nothing has been seen yet, exponents are taken against 0: all of them are of -inf
+  const float b0 = GUARD && n0 == -CUDART_INF_F ? 0.f : n0, b1 = GUARD && n1 == -CUDART_INF_F ? 0.f : n1;
+  const float a0 = fast_exp2(st.m[0] - b0), a1 = fast_exp2(st.m[1] - b1);
   st.m[0] = n0;
   st.m[1] = n1;
-  const float c0 = fv - n0, c1 = fv - n1;
+  const float c0 = fv - b0, c1 = fv - b1;
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
@@ -253,9 +264,15 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
 
 }  // namespace
 
-// NT = number of 8-head n-tiles (ceil(G / 8)); NW = warps; R = tiles (32 rows
-// of keys or of values) in a warp's ring.
-template <int D, int NT, int NW, int R, int FMT>
+// NT = number of 8-column n-tiles; NW = warps; R = tiles (32 rows of keys or of
+// values) in a warp's ring.
+//
+// CHUNK: attention of the first rows of a chunk instead of one token that is taken in.  The
+// columns of the products are then (row of the chunk, query head) pairs, up to 8 NT of them to
+// a CTA; a row at position start + t does not see the ring's slots that it has outlived (those
+// 1 .. t places after slot start mod W), and besides the tail's rows it sees the chunk's own up
+// to itself.  The cache stays as it is.
+template <int D, int NT, int NW, int R, int FMT, bool CHUNK>
 __global__ void __launch_bounds__(NW * 32, 8 / NW)
 swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
@@ -265,7 +282,8 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   unsigned char* smem_al = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024;
   float* smem = reinterpret_cast<float*>(smem_al);
 
-  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x, b = blockIdx.z;
+  const int kvh = CHUNK ? (int)blockIdx.y / p.groups : (int)blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.n_q_heads / p.n_kv_heads;
@@ -287,25 +305,37 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   wait_prior_grid();
   allow_next_grid();
   const size_t unit = (size_t)b * p.n_kv_heads + kvh;
+  // the CTA's columns: c0 .. c0 + cols - 1 of the pair's, and where column c's q and output rows are
+  const int c0 = CHUNK ? (int)(blockIdx.y % p.groups) * 8 * NT : 0;
+  const int cols = CHUNK ? min(8 * NT, p.max_tokens * G - c0) : G;
+  auto row_of = [&](int c) -> size_t {
+    if constexpr (!CHUNK) return unit * G + c;
+    const int tok = (c0 + c) / G;
+    return ((size_t)b * p.max_tokens + tok) * p.n_q_heads + (size_t)kvh * G + (c0 + c - tok * G);
+  };
   // Q is asked for before the ring's tiles, which would keep it waiting for as long as it takes to
-  // fill every ring (about 4 us).  Lane (g, t) holds head 8 nt + g.
+  // fill every ring (about 4 us).  Lane (g, t) holds column 8 nt + g.
   uint32_t qf[NT][2 * F::kKWords];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int hl = nt * 8 + g;
-    const __nv_bfloat16* qrow = p.q + (unit * G + (hl < G ? hl : 0)) * D;
+    const int c = nt * 8 + g;
+    const __nv_bfloat16* qrow = p.q + row_of(c < cols ? c : 0) * D;
 #pragma unroll
     for (int w = 0; w < F::kKWords; ++w) {
-      const uint2 x = hl < G ? ldg_stream8(qrow + key_elem<D>(t, w)) : make_uint2(0, 0);
+      const uint2 x = c < cols ? ldg_stream8(qrow + key_elem<D>(t, w)) : make_uint2(0, 0);
       qf[nt][2 * w] = x.x;
       qf[nt][2 * w + 1] = x.y;
     }
   }
   const long long pos = p.pos[b];
-  if (pos < 0) {   // every CTA of the sequence leaves here, whole clusters at a time
+  const int n_rows = CHUNK ? p.n_tokens[b] : 1;
+  if (pos < 0 || n_rows < 0 || (CHUNK && n_rows > p.max_tokens)) {
+    // every CTA of the sequence leaves here, whole clusters at a time
     if (threadIdx.x == 0) raise_status(p.status, SWA_ERR_DEVICE_ARG);
     return;
   }
+  if (CHUNK && n_rows * G <= c0) return;             // no column of this CTA has a row
+  cluster_begun_arrive();                            // waited for before the first store to a peer
   const int n_valid = (int)(pos + 1 < (long long)W ? pos + 1 : (long long)W);
   const int s_new = (int)(pos % W);
   const int blk0 = s_new / kQ8Block * kQ8Block;      // first slot of the block being filled
@@ -320,8 +350,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   const float* vsc = p.ring.v_scale + unit * n_blocks;
   __nv_bfloat16* kt = p.ring.k_tail + unit * kQ8Block * D;
   __nv_bfloat16* vt = p.ring.v_tail + unit * kQ8Block * D;
-  const __nv_bfloat16* kn = p.k_new + unit * D;
-  const __nv_bfloat16* vn = p.v_new + unit * D;
+  // the new row, or the chunk's rows, new_stride elements apart
+  const __nv_bfloat16* kn = p.k_new + (CHUNK ? ((size_t)b * p.max_tokens * p.n_kv_heads + kvh) : unit) * D;
+  const __nv_bfloat16* vn = p.v_new + (CHUNK ? ((size_t)b * p.max_tokens * p.n_kv_heads + kvh) : unit) * D;
+  const size_t new_stride = (size_t)p.n_kv_heads * D;
 
   // The warp's blocks: those of its split in turn.  Rows [first_row(x), r_end) of the block at
   // slot x are held in 8 bits and in the window; the block being filled may have none.
@@ -331,10 +363,14 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     x += NW * kQ8Block;
     return x == skip ? x + NW * kQ8Block : x;
   };
-  // The block being filled, 16 rows to a warp: keys and values are the ring's first tiles (as large as
-  // 32 rows of bytes), rows before row_new from the tail, row_new from k_new / v_new.
-  const int y0 = warp * kSub;
-  const bool has_tail = owner && y0 <= row_new;
+  // Rows in bf16, 16 at a time to the warps of one CTA of the pair: those of the block being filled
+  // (the tail's and, if one token is taken in, the new row), then those of the chunk.  Their keys and
+  // values are the ring's first tiles (16 rows of bf16 are as large as 32 rows of bytes).
+  const int old_rows = CHUNK ? row_new : row_new + 1;
+  const int old_subs = (old_rows + kSub - 1) / kSub;
+  const int subs = owner ? old_subs + (CHUNK ? (n_rows + kSub - 1) / kSub : 0) : 0;
+  static_assert(!CHUNK || 2 * ((kQ8Block / kSub + (kChunkRows + kSub - 1) / kSub + NW - 1) / NW) <= R,
+                "a warp's rows in bf16 fit its ring");
   // the tile after the last one issued: its block, which of the block's, its place in the ring
   int is_x = next_block(r_begin + (warp - NW) * kQ8Block), is_i = 0, is_at = 0;
   auto issue = [&]() {
@@ -351,22 +387,34 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     }
   };
   int x0 = is_x;
-  if (has_tail) {
-    if (lane == 0) {
+  for (int e = warp; e < subs; e += NW) {
+    const bool old = !CHUNK || e < old_subs;
+    const int first = (old ? e : e - old_subs) * kSub;               // row of the tail or of the chunk
+    const int rows = min(kSub, (old ? old_rows : n_rows) - first);
+    const uint32_t row_bytes = 2 * D;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int old = row_new - y0 < kSub ? row_new - y0 : kSub;
-        const uint32_t row_bytes = 2 * D, dst = ring + i * kTile, bar = bars + 8 * i;
-        tc::mbar_arrive_expect_tx(bar, (old < kSub ? old + 1 : kSub) * row_bytes);
-        if (old > 0) tc::bulk_load(dst, (i == 0 ? kt : vt) + (size_t)y0 * D, old * row_bytes, bar);
-        if (old < kSub) tc::bulk_load(dst + old * row_bytes, i == 0 ? kn : vn, row_bytes, bar);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t dst = ring + is_at * kTile, bar = bars + 8 * is_at;
+      if (lane == 0) tc::mbar_arrive_expect_tx(bar, rows * row_bytes);
+      __syncwarp();
+      if (old) {
+        const int held = CHUNK ? rows : min(rows, row_new - first);  // of them in the tail
+        if (lane == 0 && held > 0)
+          tc::bulk_load(dst, (i == 0 ? kt : vt) + (size_t)first * D, held * row_bytes, bar);
+        if (lane == 0 && held < rows) tc::bulk_load(dst + held * row_bytes, i == 0 ? kn : vn, row_bytes, bar);
+      } else if (lane < rows) {
+        tc::bulk_load(dst + lane * row_bytes, (i == 0 ? kn : vn) + (first + lane) * new_stride, row_bytes, bar);
       }
+      ++is_at;                                                       // at most R such tiles: is_at <= R
     }
-    is_at = 2;
   }
+  {
+    const int used = is_at;
+    if (is_at == R) is_at = 0;
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (i < R - 2 || !has_tail) issue();
+    for (int i = 0; i < R; ++i)
+      if (i >= used) issue();
+  }
   float ks = 0.f, vs = 1.f;
   if (x0 < r_end) {
     ks = ksc[x0 / kQ8Block];
@@ -374,7 +422,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
 
   // Q as the B operand of S^T = K Q^T, f16
-  float qs[NT][2];                                   // factor of the scores of heads 2t, 2t + 1
+  float qs[NT][2];                                   // factor of the scores of columns 2t, 2t + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     uint32_t m = 0;
@@ -390,6 +438,15 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     const float back = q8::exp2_int(e) * p.scale_log2;
     qs[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
     qs[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+  }
+
+  int tok[NT][2];                                    // rows of the chunk that columns 2t, 2t + 1 belong to
+  if constexpr (CHUNK) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      tok[nt][0] = (c0 + nt * 8 + 2 * t) / G;
+      tok[nt][1] = (c0 + nt * 8 + 2 * t + 1) / G;
+    }
   }
 
   State<D> st[NT];
@@ -414,17 +471,20 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     if (ok) issue();
     if (++at == R) at = 0, phase ^= 1;
   };
-  if (has_tail) {
+  for (int e = warp; e < subs && ok; e += NW) {
+    const bool old = !CHUNK || e < old_subs;
+    const int first = (old ? e : e - old_subs) * kSub;
+    const int rows = min(kSub, (old ? old_rows : n_rows) - first);
     uint32_t tile = take();
     uint32_t tk[2][2 * F::kKWords], tv[4][F::kMTiles];
     uint32_t km = 0, vm = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = y0 + i * 8 + g;
+      const int r = i * 8 + g;
 #pragma unroll
       for (int w = 0; w < F::kKWords; ++w) {
-        uint2 x = lds64(tile + (i * 8 + g) * (2 * D) + 2 * key_elem<D>(t, w));
-        if (r > row_new) x = make_uint2(0, 0);
+        uint2 x = lds64(tile + r * (2 * D) + 2 * key_elem<D>(t, w));
+        if (r >= rows) x = make_uint2(0, 0);
         tk[i][2 * w] = x.x;
         tk[i][2 * w + 1] = x.y;
         km = amax_word(amax_word(km, x.x), x.y);
@@ -435,11 +495,11 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     if (ok) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int ri = 2 * t + (i & 1) + (i >> 1) * 8, r = y0 + ri;
+        const int r = 2 * t + (i & 1) + (i >> 1) * 8;
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt) {
-          uint32_t x = lds32(tile + ri * (2 * D) + 2 * (g * (D / 8) + 2 * mt));
-          tv[i][mt] = r > row_new ? 0u : x;
+          const uint32_t x = lds32(tile + r * (2 * D) + 2 * (g * (D / 8) + 2 * mt));
+          tv[i][mt] = r >= rows ? 0u : x;
           vm = amax_word(vm, tv[i][mt]);
         }
       }
@@ -455,7 +515,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt) tv[i][mt] = bf16_to_f16(tv[i][mt], vf);
-      const bool ok0 = y0 + g <= row_new, ok1 = y0 + 8 + g <= row_new;
+      const bool ok0 = g < rows, ok1 = 8 + g < rows;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
@@ -463,10 +523,21 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         for (int w = 0; w < F::kKWords; ++w)
           mma_f16(x[0], tk[0][2 * w], tk[1][2 * w], tk[0][2 * w + 1], tk[1][2 * w + 1], qf[nt][2 * w],
                   qf[nt][2 * w + 1]);
-        if (!ok0) x[0][0] = x[0][1] = -CUDART_INF_F;
-        if (!ok1) x[0][2] = x[0][3] = -CUDART_INF_F;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          bool see0 = ok0, see1 = ok1;
+          if constexpr (CHUNK) {
+            // a row of the tail, row_new - r places before the chunk, until W tokens have come after it;
+            // a row of the chunk from itself on
+            const int tc_ = tok[nt][c], r0 = first + g, r1 = r0 + 8;
+            see0 = see0 && (old ? tc_ < W - (row_new - r0) : tc_ >= r0);
+            see1 = see1 && (old ? tc_ < W - (row_new - r1) : tc_ >= r1);
+          }
+          if (!see0) x[0][c] = -CUDART_INF_F;
+          if (!see1) x[0][2 + c] = -CUDART_INF_F;
+        }
         uint32_t pb[1][2];
-        softmax_step<D, 1>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), ve, pb);
+        softmax_step<D, 1, CHUNK>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), ve, pb);
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt)
           mma_f16(st[nt].o[mt], prmt(tv[0][mt], tv[1][mt], 0x5410), prmt(tv[0][mt], tv[1][mt], 0x7632),
@@ -516,7 +587,25 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     if (!ok) break;
 
     uint32_t pb[NT][kSubs][2];
-    if (partial) {
+    if constexpr (CHUNK) {
+      // the slot a places after s_new (round the ring) holds position start - W + a: seen by rows below a
+      const int a0 = x0 > s_new ? x0 - s_new : x0 - s_new + W;
+      if (partial || a0 < n_rows || (x0 <= s_new && s_new < x0 + kQ8Block)) {
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int slot = x0 + u * kSub + i * 8 + g, a = slot > s_new ? slot - s_new : slot - s_new + W;
+            const bool held = slot >= lo && slot < hi;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (!held || tok[nt][0] >= a) x[nt][u][2 * i] = -CUDART_INF_F;
+              if (!held || tok[nt][1] >= a) x[nt][u][2 * i + 1] = -CUDART_INF_F;
+            }
+          }
+        }
+      }
+    } else if (partial) {
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
         const int r0 = x0 + u * kSub + g, r1 = r0 + 8;
@@ -529,7 +618,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      softmax_step<D, kSubs>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks), q8::exp_of(vs),
+      softmax_step<D, kSubs, CHUNK>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks), q8::exp_of(vs),
                              pb[nt]);
 
 #pragma unroll
@@ -621,12 +710,13 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
   __syncthreads();
 
-  const int hq0 = kvh * G;
+  cluster_begun_wait();
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   const int n_cl = p.cluster ? p.n_splits : 1, rank = p.cluster ? split : 0;
-  const int per = (G * D + n_cl - 1) / n_cl;         // outputs that a CTA of the cluster merges
-  for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
+  const int per = (cols * D + n_cl - 1) / n_cl;      // outputs that a CTA of the cluster merges
+  const int live = CHUNK ? min(cols, n_rows * G - c0) : cols;   // columns with a row
+  for (int idx = threadIdx.x; idx < cols * D; idx += NW * 32) {
     const int h = idx / D, dd = idx % D;
     float M = -CUDART_INF_F;
 #pragma unroll
@@ -640,10 +730,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         O += sc * sm_o[((size_t)w * G8 + h) * kOS + dd];
       }
     }
-    const size_t bh = (size_t)b * p.n_q_heads + hq0 + h;
+    const size_t bh = row_of(h);
     if (p.n_splits == 1) {
-      store_out(p.out, bh * D + dd, O / L, p.out_f32);
-    } else if (p.cluster) {
+      if (h < live) store_out(p.out, bh * D + dd, O / L, p.out_f32);
+    } else if (CHUNK || p.cluster) {
       // each output to the CTA that merges it, m and l to all
       cl.map_shared_rank(peer_o, idx / per)[rank * per + idx % per] = O;
       if (dd < n_cl)
@@ -659,7 +749,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
 
   if (p.cluster) {
     cl.sync();   // all has been sent; every CTA of the pair's cluster comes here
-    for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < G * D; idx += NW * 32) {
+    for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < live * D; idx += NW * 32) {
       const int h = idx / D;
       float M = -CUDART_INF_F;
       for (int r = 0; r < n_cl; ++r) M = fmaxf(M, reinterpret_cast<float2*>(peer_ml)[r * G8 + h].x);
@@ -670,11 +760,11 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         L += sc * ml.y;
         O += sc * peer_o[r * per + idx - rank * per];
       }
-      store_out(p.out, ((size_t)b * p.n_q_heads + hq0) * D + idx, O / L, p.out_f32);
+      store_out(p.out, row_of(h) * D + idx % D, O / L, p.out_f32);
     }
   }
 
-  if (owner) {
+  if (!CHUNK && owner) {
     const int size = min(kQ8Block, W - blk0);
     if (row_new + 1 == size) {
       auto k_row = [&](int i) { return i == row_new ? kn : kt + (size_t)i * D; };
@@ -720,10 +810,10 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-template <int D, int NT, int NW, int R, int FMT>
+template <int D, int NT, int NW, int R, int FMT, bool CHUNK>
 cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
   constexpr int smem = q8_smem_bytes<D, NT, NW, R>();
-  auto kern = swa_q8_decode_kernel<D, NT, NW, R, FMT>;
+  auto kern = swa_q8_decode_kernel<D, NT, NW, R, FMT, CHUNK>;
   if (smem > 48 * 1024) {
     // raised once per device (the attribute persists for the process)
     static bool set[kMaxDevices] = {};
@@ -745,7 +835,7 @@ cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStre
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.n_splits, p.n_kv_heads, p.batch);
+  cfg.gridDim = dim3(p.n_splits, p.n_kv_heads * p.groups, p.batch);
   cfg.blockDim = dim3(NW * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -767,10 +857,18 @@ constexpr int kRing = 6;
 
 template <int D, int FMT>
 cudaError_t launch_f(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
+  if (p.n_tokens != nullptr) {
+    const bool few = p.max_tokens * (p.n_q_heads / p.n_kv_heads) <= 8;
+    if (p.warps == 8)
+      return few ? launch_t<D, 1, 8, kRing, FMT, true>(p, maps, stream)
+                 : launch_t<D, 2, 8, kRing, FMT, true>(p, maps, stream);
+    return few ? launch_t<D, 1, 4, kRing, FMT, true>(p, maps, stream)
+               : launch_t<D, 2, 4, kRing, FMT, true>(p, maps, stream);
+  }
   const bool wide = p.n_q_heads / p.n_kv_heads > 8;
   if (p.warps == 8)
-    return wide ? launch_t<D, 2, 8, kRing, FMT>(p, maps, stream) : launch_t<D, 1, 8, kRing, FMT>(p, maps, stream);
-  return wide ? launch_t<D, 2, 4, kRing, FMT>(p, maps, stream) : launch_t<D, 1, 4, kRing, FMT>(p, maps, stream);
+    return wide ? launch_t<D, 2, 8, kRing, FMT, false>(p, maps, stream) : launch_t<D, 1, 8, kRing, FMT, false>(p, maps, stream);
+  return wide ? launch_t<D, 2, 4, kRing, FMT, false>(p, maps, stream) : launch_t<D, 1, 4, kRing, FMT, false>(p, maps, stream);
 }
 
 template <int D>
@@ -781,10 +879,8 @@ cudaError_t launch_d(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStre
 
 }  // namespace
 
-Q8DecodeSplit q8_decode_split(int batch, int n_q_heads, int n_kv_heads, int window, int head_dim) {
-  (void)n_q_heads;
-  (void)head_dim;
-  const long long units = (long long)batch * n_kv_heads;
+Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int groups) {
+  const long long units = (long long)batch * n_kv_heads * groups;
   Q8DecodeSplit s;
   const long long n_blocks = ((long long)window + kQ8Block - 1) / kQ8Block;
   long long splits = 1;
@@ -798,6 +894,12 @@ Q8DecodeSplit q8_decode_split(int batch, int n_q_heads, int n_kv_heads, int wind
   s.cluster = s.n_splits > 1 ? 1 : 0;
   return s;
 }
+
+// Columns (rows of the chunk times query heads of a kv head) up to which a chunk is cheaper
+// here, where each 16 of them read the ring's bytes again, than written out and attended to in
+// tiles of 128 rows.
+int q8_few_columns() { return Q8_FEW; }
+int q8_chunk_groups(int columns) { return columns > 8 ? (columns + 15) / 16 : 1; }
 
 int q8_decode_box_rows() { return kTileRows; }
 
