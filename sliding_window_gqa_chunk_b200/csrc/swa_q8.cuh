@@ -94,20 +94,32 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
   return y;
 }
 
-// Rounds one block of `size` rows of K and of V (all threads of the CTA, and
-// only when all of them come here).  k_row(i) / v_row(i) give row i in bf16;
-// `dst` the block's first row in the ring.  `red` is 2 words of shared memory.
-template <int D, int FMT, typename KRow, typename VRow>
+// Rounds one block of `size` rows of K and of V (all THREADS threads of the CTA, and
+// only when all of them come here).  k_row(i) / v_row(i) give row i in bf16; `dst` the
+// block's first row in the ring.  `red` is 2 words of shared memory.  The rows stay in
+// registers between the search for the largest magnitude and the rounding.
+template <int D, int FMT, int THREADS, typename KRow, typename VRow>
 __device__ __forceinline__ void round_block(KRow k_row, VRow v_row, int size, uint8_t* k_dst, uint8_t* v_dst,
                                             float* k_scale, float* v_scale, uint32_t* red) {
   constexpr int kVecs = D / 8;
+  constexpr int kPer = (kQ8Block * kVecs + THREADS - 1) / THREADS;
   if (threadIdx.x < 2) red[threadIdx.x] = 0;
   __syncthreads();
+  uint4 k[kPer], v[kPer];
   uint32_t ka = 0, va = 0;
-  for (int i = threadIdx.x; i < size * kVecs; i += blockDim.x) {
-    const int r = i / kVecs, c = i % kVecs;
-    ka = max(ka, amax8(reinterpret_cast<const uint4*>(k_row(r))[c]));
-    va = max(va, amax8(reinterpret_cast<const uint4*>(v_row(r))[c]));
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    const int i = threadIdx.x + n * THREADS, r = i / kVecs, c = i % kVecs;
+    k[n] = v[n] = make_uint4(0, 0, 0, 0);
+    if (r < size) {
+      k[n] = reinterpret_cast<const uint4*>(k_row(r))[c];
+      v[n] = reinterpret_cast<const uint4*>(v_row(r))[c];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    ka = max(ka, amax8(k[n]));
+    va = max(va, amax8(v[n]));
   }
   ka = __reduce_max_sync(0xffffffffu, ka);
   va = __reduce_max_sync(0xffffffffu, va);
@@ -118,10 +130,12 @@ __device__ __forceinline__ void round_block(KRow k_row, VRow v_row, int size, ui
   __syncthreads();
   const int ke = scale_exp<FMT>(red[0]), ve = scale_exp<FMT>(red[1]);
   const float ki = exp2_int(-ke), vi = exp2_int(-ve);
-  for (int i = threadIdx.x; i < size * kVecs; i += blockDim.x) {
-    const int r = i / kVecs, c = i % kVecs;
-    reinterpret_cast<uint2*>(k_dst)[i] = quantise8<FMT>(reinterpret_cast<const uint4*>(k_row(r))[c], ki);
-    reinterpret_cast<uint2*>(v_dst)[i] = quantise8<FMT>(reinterpret_cast<const uint4*>(v_row(r))[c], vi);
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    const int i = threadIdx.x + n * THREADS;
+    if (i >= size * kVecs) continue;
+    reinterpret_cast<uint2*>(k_dst)[i] = quantise8<FMT>(k[n], ki);
+    reinterpret_cast<uint2*>(v_dst)[i] = quantise8<FMT>(v[n], vi);
   }
   if (threadIdx.x == 0) {
     *k_scale = exp2_int(ke);

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kAppendThreads) swa_q8_append_kernel(const Q8A
     auto k_row = [&](int i) { return t0 + i >= 0 ? kc + (size_t)(t0 + i) * row_elems : kt + (size_t)i * D; };
     auto v_row = [&](int i) { return t0 + i >= 0 ? vc + (size_t)(t0 + i) * row_elems : vt + (size_t)i * D; };
     const size_t dst = (unit * W + first) * D;
-    q8::round_block<D, FMT>(k_row, v_row, size, p.ring.k8 + dst, p.ring.v8 + dst,
+    q8::round_block<D, FMT, kAppendThreads>(k_row, v_row, size, p.ring.k8 + dst, p.ring.v8 + dst,
                             p.ring.k_scale + unit * n_blocks + j, p.ring.v_scale + unit * n_blocks + j, red);
   }
   if (blockIdx.x != 0) return;
@@ -104,21 +104,36 @@ __global__ void __launch_bounds__(kExpandThreads) swa_q8_expand_kernel(const Q8E
   allow_next_grid();
   const int j = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int W = p.window;
-  const long long s = p.start_pos[b];
-  const int n = p.n_tokens[b];
-  if (s <= 0 || n <= 0 || n > p.max_tokens) return;   // nothing is read from the ring
   const int n_blocks = (W + kQ8Block - 1) / kQ8Block;
   const int first = j * kQ8Block;
   const int size = min(kQ8Block, W - first);
+  const size_t unit = (size_t)b * p.n_kv_heads + kvh;
+  const size_t base = (unit * W + first) * D;
+  // the block's bytes are asked for together with the sequence's position, not after it
+  constexpr int kVecs = D / 16;
+  constexpr int kPer = (kQ8Block * kVecs + kExpandThreads - 1) / kExpandThreads;
+  uint4 k[kPer], v[kPer];
+#pragma unroll
+  for (int m = 0; m < kPer; ++m) {
+    const int i = threadIdx.x + m * kExpandThreads;
+    k[m] = v[m] = make_uint4(0, 0, 0, 0);
+    if (i < size * kVecs) {
+      k[m] = ldg_stream(p.ring.k8 + base + 16 * (size_t)i);
+      v[m] = ldg_stream(p.ring.v8 + base + 16 * (size_t)i);
+    }
+  }
+  const float ks = p.ring.k_scale[unit * n_blocks + j], vs = p.ring.v_scale[unit * n_blocks + j];
+  const long long s = p.start_pos[b];
+  const int n = p.n_tokens[b];
+  if (s <= 0 || n <= 0 || n > p.max_tokens) return;   // nothing is read from the ring
   const int held = s < W ? (int)s : W;                // slots [0, held) hold a position
   if (first >= (held + kKeyTile - 1) / kKeyTile * kKeyTile) return;
   const int s_slot = (int)(s % W);
   const int open = s_slot / kQ8Block == j ? s_slot - first : 0;   // rows that are in the tail
-  const size_t unit = (size_t)b * p.n_kv_heads + kvh;
-  const float ks = p.ring.k_scale[unit * n_blocks + j], vs = p.ring.v_scale[unit * n_blocks + j];
-  constexpr int kVecs = D / 16;
-  for (int i = threadIdx.x; i < size * kVecs; i += blockDim.x) {
-    const int r = i / kVecs, c = i % kVecs;
+#pragma unroll
+  for (int m = 0; m < kPer; ++m) {
+    const int i = threadIdx.x + m * kExpandThreads, r = i / kVecs, c = i % kVecs;
+    if (i >= size * kVecs) continue;
     uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;
     if (r < open) {
       const uint4* kt = reinterpret_cast<const uint4*>(p.ring.k_tail + (unit * kQ8Block + r) * D) + 2 * c;
@@ -128,14 +143,11 @@ __global__ void __launch_bounds__(kExpandThreads) swa_q8_expand_kernel(const Q8E
       v0 = vt[0];
       v1 = vt[1];
     } else if (first + r < held) {
-      const size_t src = (unit * W + first + r) * D;
-      const uint4 k = ldg_stream(p.ring.k8 + src + 16 * c), v = ldg_stream(p.ring.v8 + src + 16 * c);
-      expand16<FMT>(k, ks, k0, k1);
-      expand16<FMT>(v, vs, v0, v1);
+      expand16<FMT>(k[m], ks, k0, k1);
+      expand16<FMT>(v[m], vs, v0, v1);
     }
-    const size_t dst = (unit * W + first + r) * D;
-    uint4* ko = reinterpret_cast<uint4*>(p.k_out + dst) + 2 * c;
-    uint4* vo = reinterpret_cast<uint4*>(p.v_out + dst) + 2 * c;
+    uint4* ko = reinterpret_cast<uint4*>(p.k_out + base) + 2 * (size_t)i;
+    uint4* vo = reinterpret_cast<uint4*>(p.v_out + base) + 2 * (size_t)i;
     ko[0] = k0;
     ko[1] = k1;
     vo[0] = v0;

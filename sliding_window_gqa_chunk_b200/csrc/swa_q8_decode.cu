@@ -570,17 +570,22 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         for (int i = 0; i < 2; ++i) load_key8<D>(kw[s][i], tile, s * kSub + i * 8 + g, t);
       done();
 #pragma unroll
-      for (int s = 0; s < kTileSubs; ++s) {
-        const int u = h * kTileSubs + s;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt][u][0] = x[nt][u][1] = x[nt][u][2] = x[nt][u][3] = 0.f;
+        for (int s = 0; s < kTileSubs; ++s)
+          x[nt][h * kTileSubs + s][0] = x[nt][h * kTileSubs + s][1] = x[nt][h * kTileSubs + s][2] =
+              x[nt][h * kTileSubs + s][3] = 0.f;
+      // the sums of the tile's two mma blocks (and n-tiles) are independent chains
 #pragma unroll
-        for (int w = 0; w < F::kKWords; ++w) {
+      for (int w = 0; w < F::kKWords; ++w) {
+#pragma unroll
+        for (int s = 0; s < kTileSubs; ++s) {
           uint32_t a0, a1, a2, a3;
           q8::unpack4<FMT>(kw[s][0][w], a0, a2);
           q8::unpack4<FMT>(kw[s][1][w], a1, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt][u], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(x[nt][h * kTileSubs + s], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
         }
       }
     }
@@ -770,7 +775,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       auto k_row = [&](int i) { return i == row_new ? kn : kt + (size_t)i * D; };
       auto v_row = [&](int i) { return i == row_new ? vn : vt + (size_t)i * D; };
       const size_t dst = (unit * W + blk0) * D;
-      q8::round_block<D, FMT>(k_row, v_row, size, p.ring.k8 + dst, p.ring.v8 + dst,
+      q8::round_block<D, FMT, NW * 32>(k_row, v_row, size, p.ring.k8 + dst, p.ring.v8 + dst,
                               p.ring.k_scale + unit * n_blocks + blk0 / kQ8Block,
                               p.ring.v_scale + unit * n_blocks + blk0 / kQ8Block, red);
     } else if (warp == 0) {

@@ -54,7 +54,7 @@ __device__ __forceinline__ void turn(uint4& a, uint4& b, const float (&cs)[8], c
 
 // TOK tokens (of all B * T, numbered through) per CTA.
 template <bool INTER, int TOK>
-__global__ void __launch_bounds__(kThreads) swa_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 5) swa_rope_kernel(const RopeParams p) {
   __shared__ float2 ang[TOK][kMaxPairs];
   __shared__ int live[TOK];
   wait_prior_grid();
@@ -104,14 +104,17 @@ __global__ void __launch_bounds__(kThreads) swa_rope_kernel(const RopeParams p) 
   // first elements of the unit's two pieces
   const int e0 = (!INTER && turned) ? 8 * c : 16 * c;
   const int e1 = (!INTER && turned) ? p.rotary_dim / 2 + 8 * c : 16 * c + 8;
-  const int heads = p.n_q_heads + p.n_kv_heads;
-  for (int h = blockIdx.y * lanes + lane; h < heads; h += gridDim.y * lanes) {
-    const bool is_q = h < p.n_q_heads;
+  // where head h of the token's row is: k's heads are counted on from q's
+  const int D = p.head_dim, Hq = p.n_q_heads, heads = Hq + p.n_kv_heads;
+  const __nv_bfloat16* q = p.q + tok * p.q_stride;
+  const __nv_bfloat16* k = p.k + (tok * p.k_stride - Hq * D);
+  __nv_bfloat16* q_out = p.q_out + (size_t)tok * Hq * D;
+  __nv_bfloat16* k_out = p.k_out + ((int64_t)tok * p.n_kv_heads - Hq) * D;
+  for (int h = lane; h < heads; h += lanes) {
+    const bool is_q = h < Hq;
     if (!turned && (is_q ? p.q_in_place : p.k_in_place)) continue;
-    const int hh = is_q ? h : h - p.n_q_heads;
-    const __nv_bfloat16* src = (is_q ? p.q + tok * p.q_stride : p.k + tok * p.k_stride) + (size_t)hh * p.head_dim;
-    __nv_bfloat16* dst = (is_q ? p.q_out + (size_t)tok * p.n_q_heads * p.head_dim
-                               : p.k_out + (size_t)tok * p.n_kv_heads * p.head_dim) + (size_t)hh * p.head_dim;
+    const __nv_bfloat16* src = (is_q ? q : k) + h * D;
+    __nv_bfloat16* dst = (is_q ? q_out : k_out) + h * D;
     uint4 a = *reinterpret_cast<const uint4*>(src + e0), b = *reinterpret_cast<const uint4*>(src + e1);
     if (turned) turn<INTER>(a, b, cs, sn);
     *reinterpret_cast<uint4*>(dst + e0) = a;
