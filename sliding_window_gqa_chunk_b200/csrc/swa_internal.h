@@ -178,7 +178,7 @@ struct Q8DecodeParams {
 struct Q8DecodeSplit {
   int n_splits, slots_per_split, warps, cluster;
 };
-Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int groups);
+Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int groups, bool chunk);
 // Chunks of at most this many columns (rows x query heads of a kv head) go through launch_q8_decode
 // too, with q, k, v and out as in the prefill and start positions as pos.
 int q8_few_columns();

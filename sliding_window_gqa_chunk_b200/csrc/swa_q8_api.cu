@@ -155,7 +155,7 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
     d.n_tokens = n_tokens;
     d.max_tokens = max_tokens;
     d.groups = swa::q8_chunk_groups(max_tokens * columns_per_row);
-    const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, d.groups);
+    const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, d.groups, true);
     return launch_over_ring(d, dims, cache, out, q, k, v, start_pos, sp, stream, "swa_q8_prefill_chunk");
   }
   // the prefill's own limit, before the ring is expanded: a refused call enqueues nothing
@@ -182,7 +182,7 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
 
 size_t swa_q8_decode_workspace_size(const swa_dims* dims) {
   if (check_q8_dims(dims) != SWA_OK) return 0;
-  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1);
+  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1, false);
   if (sp.n_splits == 1 || sp.cluster) return 16;  // nothing needed; a non-zero size keeps callers simple
   return (size_t)dims->batch * dims->n_q_heads * sp.n_splits * (dims->head_dim + 2) * sizeof(float);
 }
@@ -201,7 +201,7 @@ int swa_q8_decode(const swa_dims* dims, void* out, const void* q, const void* k_
   if (workspace_bytes < need)
     return swa::api_fail(SWA_ERR_WORKSPACE_TOO_SMALL, "q8 decode workspace of %zu bytes, %zu needed",
                          workspace_bytes, need);
-  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1);
+  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1, false);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = p.ws_o + (size_t)dims->batch * dims->n_q_heads * sp.n_splits * dims->head_dim;
   p.n_tokens = nullptr;

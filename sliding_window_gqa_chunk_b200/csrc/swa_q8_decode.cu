@@ -1,38 +1,43 @@
-// swa_q8_decode.cu - single-token decode over the 8-bit rolling cache.
+// swa_q8_decode.cu - attention of one token, or of a chunk's few rows, over the 8-bit
+// rolling cache.
 //
-// The step is the bf16 decode's (a query attends over the min(pos + 1, W)
-// positions (pos - W, pos]), over half the bytes: every (sequence, kv head)
-// streams W slots x d x 1 B of keys and the same of values.  One warp handles
-// all G query heads of its kv head, and the dot products run on mma.sync
-// m16n8k16 in f16 with fp32 sums, in which every 8-bit number is exact:
+// A decode step attends over the min(pos + 1, W) positions (pos - W, pos], as the
+// bf16 one does, over half the bytes: every (sequence, kv head) streams W slots x
+// d x 1 B of keys and the same of values.  One warp handles all G query heads of its
+// kv head, and the dot products run on mma.sync m16n8k16 in f16 with fp32 sums, in
+// which every 8-bit number is exact:
 //
 //   S^T[slot][head] = K[slot][:] . Q[head][:]        (M = 16 slots, N = 8 heads, K = d)
 //   O^T[d][head]   += V^T[d][slot] . P^T[slot][head] (M = 16 d, N = 8 heads, K = 16 slots)
 //
-// tcgen05 has nothing to offer here: at G = 4 the tensor work is a few percent
-// of the time that the bytes take, and its operands would have to be written
-// back to shared memory in 16 bits.
+// tcgen05 has nothing to offer here: at G = 4 the tensor pipe is busy for a fifth of
+// the time that the bytes take, and its operands would have to be written back to
+// shared memory in 16 bits.
 //
-// Scales.  A block's key scale multiplies its scores.  Its value scale 2^v is
-// put into the exponent of the softmax: with x the score in log2 units, the
-// weight of a slot is w = 2^(x + v - m), where the running m is the maximum of
-// x + v rather than of x.  The numbers of a block's values always reach the top
-// of their format, so w orders the slots by what they can add to the output
-// and is at most 1: rounding w to f16 loses what is below 2^-24 of the largest
-// such addition.  The softmax sum is that of 2^(x - m) = w 2^-v, in fp32.
-// Q goes to f16 with one power of two for each head (its largest magnitude to
-// [2^14, 2^15)): its 8 bits are kept in all elements above 2^-28 of the
-// largest.  The rows of the block being filled (at most 64, in bf16) go
-// through the same products, 16 rows with a power of two of their own at a time.
+// Scales.  A block's key scale multiplies its scores.  Its value scale 2^v is put into
+// the exponent of the softmax: with x the score in log2 units, the weight of a slot is
+// w = 2^(x + v - m + 15), where the running m is the maximum of x + v rather than of x.
+// The numbers of a block's values always reach the top of their format, so w orders the
+// slots by what they can add to the output and is at most 2^15: f16 keeps 11 bits of the
+// weights down to 2^-29 of the largest.  The softmax sum is that of 2^(x - m) =
+// w 2^(-v - 15), in fp32.  Q goes to f16 with one power of two for each head (its largest
+// magnitude to [2^14, 2^15)): its 8 bits are kept in all elements above 2^-28 of the
+// largest.  The rows of the block being filled (at most 64, in bf16) go through the same
+// products, 16 rows with a power of two of their own at a time.
 //
-// Work split: grid (n_splits, Hkv, B); the warps of a CTA take pieces of 16 or
-// 32 slots (never across a scale block) in turn, then merge their (m, l, O) in
-// shared memory, and the splits of a pair merge through distributed shared
-// memory (thread-block cluster) or through the workspace and a second kernel.
-// The CTA whose split holds slot pos mod W takes the rows of the tail into its
-// sweep, writes the new row there or, if it is its block's last, rounds the
-// block into the ring.  That block's old rows are then all out of the window,
-// so no CTA reads what is being written.
+// Bytes.  The bound is HBM: 538 MB for 64 sequences of W = 4096 with 8 kv heads of 128
+// take 88 us (6.1 TB/s of 6.56 measured for a copy).  Each warp streams its blocks through
+// a ring of its own in shared memory, 6 tiles of 32 rows, filled by TMA and freed by the
+// warp when the tile is in registers; no warp waits for another before the merge.  8 warps
+// an SM keep 192 KB in flight.  Loads into registers with 12 warps an SM took 172 us; rings of
+// 12 KB for 16 warps 100 us (the arithmetic of a block is as long as a ring).
+//
+// Work split: grid (n_splits, Hkv, B); the warps of a CTA take the 64-slot blocks of its split
+// in turn and merge their (m, l, O) in shared memory, and the splits of a pair merge through
+// distributed shared memory (thread-block cluster) or through the workspace and a second
+// kernel.  The CTA whose split holds slot pos mod W takes the rows of the tail into its sweep,
+// writes the new row there or, if it is its block's last, rounds the block into the ring.  That
+// block's old rows are then all out of the window, so no CTA reads what is being written.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,9 +50,6 @@
 
 namespace swa {
 
-#ifndef Q8_FEW
-#define Q8_FEW 128
-#endif
 namespace {
 
 constexpr int kSub = 16;            // slots of one mma block
@@ -56,7 +58,9 @@ constexpr int kTileRows = 32;       // rows of a TMA tile
 constexpr int kTileSubs = kTileRows / kSub;
 constexpr int kTiles = kQ8Block / kTileRows;  // tiles of a block's keys (and of its values)
 constexpr int kMaxCluster = 8;      // portable cluster size
-constexpr int kChunkRows = 128;     // rows of the longest chunk that comes here
+constexpr float kWeightExp = 15.f;  // the largest weight is 2^15
+constexpr float kWeightUnit = 1.f / 32768.f;
+constexpr int kChunkRows = 128;     // columns, and so rows, of the largest chunk that comes here
 
 // Row fragments of a lane: bytes of a key row (D / 4) and of a value row (D / 8).
 template <int D>
@@ -238,7 +242,7 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
   const float a0 = fast_exp2(st.m[0] - b0), a1 = fast_exp2(st.m[1] - b1);
   st.m[0] = n0;
   st.m[1] = n1;
-  const float c0 = fv - b0, c1 = fv - b1;
+  const float c0 = fv + kWeightExp - b0, c1 = fv + kWeightExp - b1;
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
@@ -249,8 +253,8 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
     pb[u][0] = movmatrix_trans(pack_f16x2(p0, p1));
     pb[u][1] = movmatrix_trans(pack_f16x2(p2, p3));
   }
-  st.l[0] = st.l[0] * a0 + s0 * inv;
-  st.l[1] = st.l[1] * a1 + s1 * inv;
+  st.l[0] = st.l[0] * a0 + s0 * kWeightUnit * inv;
+  st.l[1] = st.l[1] * a1 + s1 * kWeightUnit * inv;
   if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {   // a maximum moved
 #pragma unroll
     for (int mt = 0; mt < Q8Frag<D>::kMTiles; ++mt) {
@@ -737,7 +741,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     }
     const size_t bh = row_of(h);
     if (p.n_splits == 1) {
-      if (h < live) store_out(p.out, bh * D + dd, O / L, p.out_f32);
+      if (h < live) store_out(p.out, bh * D + dd, O * kWeightUnit / L, p.out_f32);
     } else if (CHUNK || p.cluster) {
       // each output to the CTA that merges it, m and l to all
       cl.map_shared_rank(peer_o, idx / per)[rank * per + idx % per] = O;
@@ -765,7 +769,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         L += sc * ml.y;
         O += sc * peer_o[r * per + idx - rank * per];
       }
-      store_out(p.out, row_of(h) * D + idx % D, O / L, p.out_f32);
+      store_out(p.out, row_of(h) * D + idx % D, O * kWeightUnit / L, p.out_f32);
     }
   }
 
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(D < 32 ? 32 : D) swa_q8_decode_combine_kernel(
     L += sc * ml[2 * s + 1];
     O += sc * op[(size_t)s * D];
   }
-  store_out(p.out, bh * D + dd, O / L, p.out_f32);
+  store_out(p.out, bh * D + dd, O * kWeightUnit / L, p.out_f32);
 }
 
 namespace {
@@ -859,6 +863,11 @@ cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStre
 
 // 8 warps an SM, with 24 KB of tiles in flight for each.
 constexpr int kRing = 6;
+constexpr int kSms = 148;
+// Blocks of a window from which the pairs, where there are fewer than 148 / 8, go over all SMs and are
+// merged by a second kernel, not over clusters of 8: 8 pairs of 2048 blocks take 55 us and 74, of 512
+// blocks 23 either way, of 64 blocks 10.7 and 8.1.
+constexpr int kLongBlocks = 512;
 
 template <int D, int FMT>
 cudaError_t launch_f(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
@@ -884,26 +893,44 @@ cudaError_t launch_d(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStre
 
 }  // namespace
 
-Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int groups) {
+// How the pairs (of a chunk: the CTAs' shares of their columns) are spread over the SMs; a function
+// of the shape alone.  Measured at 64 blocks a pair (W = 4096, d = 128, e4m3):
+//  - fewer than 148: CTAs of 8 warps, one an SM, and the blocks of a pair over the CTAs of a cluster
+//    of at most 8, or, for one token in a long window, over all SMs and merged by a second kernel;
+//  - more: a CTA to a pair, either of 4 warps, two to an SM at once, or of 8.  A wave of the latter
+//    takes 22.5 us; one of the former 46 us if it is full, 33 us if it holds at most a CTA an SM and
+//    the more the nearer it is to full.  So 320 pairs take 68 us with 8 warps and 82 with 4, 512
+//    pairs 92 and 88, 768 pairs 132 and 131, 1184 pairs 195 and 201.
+Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int groups, bool chunk) {
   const long long units = (long long)batch * n_kv_heads * groups;
-  Q8DecodeSplit s;
   const long long n_blocks = ((long long)window + kQ8Block - 1) / kQ8Block;
+  Q8DecodeSplit s;
   long long splits = 1;
-  if (units < 148) splits = 148 / units;
-  s.warps = units < 148 ? 8 : 4;
-  if (splits > kMaxCluster) splits = kMaxCluster;
-  if (splits > n_blocks) splits = n_blocks;
+  s.cluster = 0;
+  if (units < kSms) {
+    s.warps = 8;
+    splits = kSms / units;
+    if (splits > kMaxCluster && (chunk || n_blocks < kLongBlocks)) splits = kMaxCluster;
+    if (splits > n_blocks) splits = n_blocks;
+    s.cluster = splits <= kMaxCluster;
+  } else {
+    const long long rest = units % (2 * kSms);
+    const double four = 2.04 * (double)(units / (2 * kSms)) +
+                        (rest > kSms ? 1.47 + 0.57 * (double)(rest - kSms) / kSms : rest > 0 ? 1.47 : 0.0);
+    s.warps = (double)((units + kSms - 1) / kSms) < four ? 8 : 4;
+  }
   const long long per = (n_blocks + splits - 1) / splits;
   s.slots_per_split = (int)(per * kQ8Block);
   s.n_splits = (int)((n_blocks + per - 1) / per);
-  s.cluster = s.n_splits > 1 ? 1 : 0;
+  if (s.n_splits == 1) s.cluster = 0;
   return s;
 }
 
-// Columns (rows of the chunk times query heads of a kv head) up to which a chunk is cheaper
-// here, where each 16 of them read the ring's bytes again, than written out and attended to in
-// tiles of 128 rows.
-int q8_few_columns() { return Q8_FEW; }
+// Columns (rows of the chunk times query heads of a kv head) up to which a chunk goes straight over
+// the ring's bytes, which each 16 of them read again, and is not written out in bf16 and attended to in
+// tiles of 128 rows.  At W = 4096, 32 query heads over 8, d = 128: 16 columns 35 us and 205 for 16
+// sequences; 128 columns 217 and 209 for 16 sequences, 23 and 48 for one.
+int q8_few_columns() { return kChunkRows; }
 int q8_chunk_groups(int columns) { return columns > 8 ? (columns + 15) / 16 : 1; }
 
 int q8_decode_box_rows() { return kTileRows; }

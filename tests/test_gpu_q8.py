@@ -4,13 +4,13 @@ The cache's contents (8-bit numbers, scales, tails) are compared exactly: scales
 are powers of two and every rounding is to nearest even, so there is one right
 answer.  Attention outputs are held to bounds that follow from the arithmetic:
 
-* decode rounds the weights w <= 1 to f16 (half a step: 2^-11 of the weight, or
-  2^-25 where it is subnormal), and does the rest in fp32: the scores (d products,
-  d 2^-24 of their sizes' sum), exp2 (2^-22) and the sums.  For the scores here
-  (|x| below 2^4) these stay within another 2^-11.  So |out - ref| <= 2^-10 S, with S
-  the weighted mean of |v|, plus n 2^-23 of the largest |v| for the subnormal
-  weights (a weight is relative to the largest product of weight and value scale, and
-  no value exceeds 448 / 224 times what its block's largest one says).
+* decode (and a chunk of few rows) rounds the weights to f16 (half a step: 2^-11 of the
+  weight, or 2^-25 where it is subnormal, the largest being 2^15 or 2^14 at least), and does
+  the rest in fp32: the scores (d products, d 2^-24 of their sizes' sum), exp2 (2^-22) and
+  the sums.  For the scores here (|x| below 2^4) these stay within another 2^-11.  So
+  |out - ref| <= 2^-10 S, with S the weighted mean of |v|, plus n 2^-23 of the largest |v|
+  for the subnormal weights (a weight is relative to the largest product of weight and value
+  scale, and no value exceeds 448 / 224 times what its block's largest one says; 2^-37 would do).
 * prefill rounds the weights to bf16 (2^-8), the rest as above: (2^-8 + 2^-10) S.
 * bf16 output adds half a step, 2^-8 of the output.
 """
@@ -158,6 +158,8 @@ DECODE = [
     (1, 32, 8, 128, 1024, [2047], 2),              # clusters of 8
     (40, 4, 4, 16, 200, [i * 13 for i in range(40)], 2),    # 160 pairs: splits merged through the workspace
     (150, 2, 1, 64, 64, list(range(150)), 2),
+    (300, 1, 1, 16, 130, list(range(300)), 2),              # 300 pairs: two CTAs an SM
+    (7, 3, 3, 16, 70, [0, 1, 5, 63, 64, 69, 70], 8),        # a last block of 6 slots, filled up and begun
 ]
 
 
@@ -249,6 +251,13 @@ def test_decode_does_not_read_masked_rows():
     (2, 4, 4, 128, 1000, 130, [130, 990], [130, 130]),
     (4, 16, 2, 128, 640, 4, [1, 639, 640, 1300], [4, 4, 2, 3]),   # a few tokens each
     (3, 14, 2, 64, 300, 9, [0, 5, 700], [9, 9, 9]),
+    (2, 2, 2, 64, 64, 64, [64, 31], [64, 64]),              # 64 columns of a window of one block: every row outlives one
+    (3, 4, 4, 16, 70, 70, [0, 69, 211], [70, 33, 70]),      # a short last block, rows that see only the chunk's end
+    (2, 16, 1, 64, 130, 8, [129, 260], [8, 5]),             # 128 columns: 8 CTAs share them
+    (1, 3, 1, 128, 1000, 2, [999], [2]),                    # 6 columns, clusters
+    (160, 2, 1, 16, 64, 3, list(range(160)), [i % 4 for i in range(160)]),   # more pairs than SMs, some without rows
+    (2, 1, 1, 128, 200, 128, [63, 137], [128, 128]),        # the longest chunk that goes over the bytes
+    (2, 1, 1, 128, 200, 129, [63, 137], [129, 129]),        # and the shortest that does not
 ])
 def test_prefill_matches_the_oracle(fmt, B, Hq, H, d, W, T, starts, counts):
     out = "bf16" if fmt == "int8" else "f32"
@@ -268,6 +277,132 @@ def test_prefill_matches_the_oracle(fmt, B, Hq, H, d, W, T, starts, counts):
             if n:
                 close(o[b, :n], want[b, :n], spread[b, :n], PREFILL_REL, 1e-6, f"sequence {b}", out)
     same_cache(cache, ref)
+    swa.device_status()
+
+
+def test_decode_of_a_long_window_goes_over_all_sms():
+    """More than 512 blocks and one pair: partials in the workspace, merged by the second kernel."""
+    B, Hq, H, d, W = 1, 4, 1, 16, 32768 + 70
+    g = torch.Generator().manual_seed(77)
+    dims, cache, ref = make(B, Hq, H, d, W, "int8")
+    assert swa.decode_workspace_size_q8(dims) > 16
+    pos = fill(dims, cache, ref, [W + 100], g, W)
+    ws = swa.decode_workspace_q8(dims, DEV).fill_(255)       # what it holds before does not matter
+    for i in range(2):
+        q, k, v = torch.randn(B, Hq, d, generator=g).to(torch.bfloat16), rows(g, B, H, d), rows(g, B, H, d)
+        o = torch.empty((B, Hq, d), dtype=torch.float32, device=DEV)
+        swa.decode_q8(dims, o, q.to(DEV), k.to(DEV), v.to(DEV), cache, i32(pos), ws)
+        want, spread = q8.decode(ref, q, k, v, pos, dims.scale)
+        # the subnormal weights' part, W 2^-37 of the largest |v| (see above)
+        close(o, want, spread, DECODE_REL, W * 2.0 ** -37 * 500, f"step {i}")
+        pos = [p + 1 for p in pos]
+    swa.device_status()
+
+
+def test_decode_writes_nothing_else():
+    """Bytes around every tensor that a step writes, and the rows that it must leave, stay as they were."""
+    B, Hq, H, d, W = 3, 4, 2, 64, 100
+    dims = swa.Dims(B, Hq, H, d, W, 0.125, "bf16")
+    g = torch.Generator(device=DEV).manual_seed(6)
+    shapes = [((B, H, W, d), torch.int8), ((B, H, W, d), torch.int8), ((B, H, 2), torch.float32), ((B, H, 2), torch.float32),
+              ((B, H, 64, d), torch.bfloat16), ((B, H, 64, d), torch.bfloat16), ((B, Hq, d), torch.bfloat16)]
+    guarded = []
+    for shape, dtype in shapes:
+        n = math.prod(shape)
+        whole = torch.full((n + 512,), 1, dtype=dtype, device=DEV)
+        guarded.append((whole, whole[256:256 + n].view(shape)))
+    cache, out = swa.CacheQ8(*[x[1] for x in guarded[:6]]), guarded[6][1]
+    ws = swa.decode_workspace_q8(dims, DEV)
+    pos = [0, 63, 250]          # into the tail; fills a block of 64; into the tail of a running ring
+    before = [x[0].clone() for x in guarded]
+    rnd = lambda h: torch.randn(B, h, d, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    k, v = rnd(H), rnd(H)
+    swa.decode_q8(dims, out, rnd(Hq), k, v, cache, i32(pos), ws)
+    for i, ((whole, inner), old) in enumerate(zip(guarded, before)):
+        n = inner.numel()
+        assert torch.equal(whole[:256], old[:256]) and torch.equal(whole[256 + n:], old[256 + n:])
+        was = old[256:256 + n].view(inner.shape)
+        if i < 2:
+            assert torch.equal(inner[0], was[0]) and torch.equal(inner[2], was[2]) and torch.equal(inner[1, :, 64:], was[1, :, 64:])
+        elif i < 4:
+            assert torch.equal(inner[0], was[0]) and torch.equal(inner[2], was[2]) and torch.equal(inner[1, :, 1], was[1, :, 1])
+        elif i < 6:
+            new = k if i == 4 else v
+            want = was.clone()
+            want[0, :, 0], want[2, :, 50] = new[0], new[2]
+            assert torch.equal(inner, want)
+    swa.device_status()
+
+
+def test_two_streams_with_their_own_workspaces():
+    """Two layers' steps at the same time on two streams give what they give one after the other."""
+    B, Hq, H, d, W = 4, 8, 2, 128, 512
+    dims = swa.Dims(B, Hq, H, d, W, 0.1, "f32")
+    g = torch.Generator(device=DEV).manual_seed(12)
+
+    def layer():
+        cache = swa.new_cache_q8(dims, "e4m3", DEV)
+        k, v = (torch.randn(B, W, H, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+        swa.cache_append_q8(dims, cache, k, v, i32([0] * B), i32([W] * B))
+        q = torch.randn(B, Hq, d, generator=g, device=DEV).to(torch.bfloat16)
+        return cache, q, k[:, 3].contiguous(), v[:, 5].contiguous()
+
+    layers, pos = [layer() for _ in range(2)], i32([W] * B)
+    alone, together = [], []
+    for cache, q, k, v in layers:
+        o = torch.empty((B, Hq, d), device=DEV)
+        swa.decode_q8(dims, o, q, k, v, cache, pos, swa.decode_workspace_q8(dims, DEV))
+        alone.append(o)
+    torch.cuda.synchronize()
+    streams, spaces = [torch.cuda.Stream() for _ in range(2)], [swa.decode_workspace_q8(dims, DEV) for _ in range(2)]
+    outs = [torch.empty((B, Hq, d), device=DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):          # the same step again: the row is already there
+        for (cache, q, k, v), s, ws, o in zip(layers, streams, spaces, outs):
+            swa.decode_q8(dims, o, q, k, v, cache, pos, ws, stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, outs):
+        assert torch.equal(a, b)
+    swa.device_status()
+
+
+def test_binding_refuses_what_does_not_fit():
+    dims, cache, _ = make(2, 4, 2, 64, 128, "e4m3")
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device=DEV)  # noqa: E731
+    ws, pos, o = swa.decode_workspace_q8(dims, DEV), i32([0, 0]), z(2, 4, 64, dt=torch.float32)
+    q, k = z(2, 4, 64), z(2, 2, 64)
+    good = dict(out=o, q=q, k_new=k, v_new=k.clone(), cache=cache, pos=pos, workspace=ws)
+    swa.decode_q8(dims, **good)
+    for name, bad in (("out", z(2, 4, 64)), ("q", z(2, 4, 32)), ("q", q.float()), ("k_new", z(2, 4, 64)), ("v_new", z(2, 2, 64).cpu()),
+                      ("k_new", z(2, 64, 2).transpose(1, 2)), ("pos", pos.long()), ("pos", i32([0])), ("workspace", ws.cpu())):
+        with pytest.raises(ValueError, match=name):
+            swa.decode_q8(dims, **{**good, name: bad})
+    other = swa.Dims(2, 4, 2, 64, 192, 0.1, "f32")
+    with pytest.raises(ValueError, match="cache"):
+        swa.decode_q8(other, **good)
+    with pytest.raises(ValueError, match="k_scale"):
+        swa.CacheQ8(cache.k, cache.v, cache.k_scale[:, :, :1].contiguous(), cache.v_scale, cache.k_tail, cache.v_tail)
+    with pytest.raises(ValueError, match="v: "):
+        swa.CacheQ8(cache.k, cache.v.view(torch.int8), cache.k_scale, cache.v_scale, cache.k_tail, cache.v_tail)
+    with pytest.raises(swa.SwaError) as e:
+        swa.prefill_chunk_q8(dims, z(2, 1, 4, 64, dt=torch.float32), z(2, 1, 4, 64), z(2, 1, 2, 64), z(2, 1, 2, 64), cache, pos, pos, ws)
+    assert e.value.code == swa.SWA_ERR_WORKSPACE_TOO_SMALL
+    with pytest.raises(ValueError, match="n_tokens"):
+        swa.cache_append_q8(dims, cache, z(2, 1, 2, 64), z(2, 1, 2, 64), pos, i32([1]))
+    with pytest.raises(swa.SwaError):
+        swa.cache_append_q8(dims, cache, z(2, 129, 2, 64), z(2, 129, 2, 64), pos, pos)
+    spec = swa.new_rope(64, device=DEV)
+    x, y = z(2, 3, 4, 64), z(2, 3, 2, 64)
+    with pytest.raises(ValueError, match="k and k_out"):
+        swa.rope(dims, spec, x, None, x, y, pos)
+    with pytest.raises(ValueError, match="q: "):
+        swa.rope(dims, spec, x, y, z(2, 3, 4, 128)[..., ::2], y, pos)
+    with pytest.raises(ValueError, match="q_out"):
+        swa.rope(dims, spec, z(2, 3, 64, 4).transpose(2, 3), y, x, y, pos)
+    with pytest.raises(swa.SwaError):
+        swa.rope(dims, swa.new_rope(8, device=DEV), x, y, x, y, pos)
+    with pytest.raises(swa.SwaError):      # one row for all tokens: rows on top of one another
+        swa.rope(dims, spec, x, y, z(1, 1, 4, 64).expand(2, 3, 4, 64), y, pos)
     swa.device_status()
 
 
