@@ -146,15 +146,16 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
   if (workspace_bytes < need)
     return swa::api_fail(SWA_ERR_WORKSPACE_TOO_SMALL, "q8 prefill workspace of %zu bytes, %zu needed",
                          workspace_bytes, need);
-  const int columns_per_row = dims->n_q_heads / dims->n_kv_heads;
-  if ((long long)max_tokens * columns_per_row <= swa::q8_few_columns()) {
+  const long long columns = (long long)max_tokens * (dims->n_q_heads / dims->n_kv_heads);
+  const int groups = columns <= swa::q8_few_columns() ? swa::q8_chunk_groups((int)columns) : 0;
+  if (groups > 0 && (long long)dims->n_kv_heads * groups <= 65535) {   // CTAs along the grid's second axis
     // a few rows: straight over the ring's bytes
     swa::Q8DecodeParams d;
     d.ring = p.ring;
     d.ws_o = d.ws_ml = nullptr;
     d.n_tokens = n_tokens;
     d.max_tokens = max_tokens;
-    d.groups = swa::q8_chunk_groups(max_tokens * columns_per_row);
+    d.groups = groups;
     const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, d.groups, true);
     return launch_over_ring(d, dims, cache, out, q, k, v, start_pos, sp, stream, "swa_q8_prefill_chunk");
   }

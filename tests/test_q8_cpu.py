@@ -123,9 +123,10 @@ def test_bad_counts(lib):
         assert append(lib, **kw) == swa.SWA_ERR_INVALID_ARG
     assert prefill(lib, s=None) == swa.SWA_ERR_INVALID_ARG
     assert decode(lib, pos=FAKE + 2) == swa.SWA_ERR_INVALID_ARG
-    # more query tiles than the prefill takes: refused before the ring is written out
-    big = dims(batch=65535, n_q_heads=16384, n_kv_heads=16384, head_dim=16, window=4)
-    assert prefill(lib, d=big, T=1, size=1 << 62) == swa.SWA_ERR_UNSUPPORTED
+    # more query tiles than the prefill takes: refused before the ring is written out (129 rows, as up to
+    # 128 columns go another way)
+    big = dims(batch=65535, n_q_heads=16384, n_kv_heads=16384, head_dim=16, window=200)
+    assert prefill(lib, d=big, T=129, size=1 << 62) == swa.SWA_ERR_UNSUPPORTED
 
 
 def test_rope_refusals(lib):
