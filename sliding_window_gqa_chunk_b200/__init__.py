@@ -102,6 +102,17 @@ class _CRope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float)]
 
 
+# What the module _native reads of a CacheQ8 and of a Rope, at the address they keep: the C
+# structure, and what it checks a call's other tensors against.
+class _CacheRecord(ctypes.Structure):
+    _fields_ = [("c", _CCacheQ8), ("batch", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("device", ctypes.c_int32)]
+
+
+class _RopeRecord(ctypes.Structure):
+    _fields_ = [("c", _CRope), ("device", ctypes.c_int32)]
+
+
 @dataclasses.dataclass(frozen=True)
 class Dims:
     """Shape of one attention layer (mirrors ``swa_dims``)."""
@@ -119,8 +130,15 @@ class Dims:
                       float(self.scale), _DTYPES[self.out_dtype])
 
     @functools.cached_property
-    def _ref(self):
-        return ctypes.byref(self.c())
+    def _record(self) -> _CDims:
+        return self.c()
+
+    @functools.cached_property
+    def _dims_addr(self) -> int:
+        return ctypes.addressof(self._record)
+
+    def __reduce__(self):       # a copy makes its own record
+        return Dims, tuple(getattr(self, f.name) for f in dataclasses.fields(self))
 
     @property
     def torch_out_dtype(self) -> torch.dtype:
@@ -301,11 +319,28 @@ def device_status(stream=None) -> None:
 # ---- the 8-bit rolling cache and the rotary positions ----
 #
 # These calls check their tensors (type, shape, device, density) before anything
-# is launched, and run on the device that the tensors are on.
+# is launched, and run on the device that the tensors are on.  The checks and the
+# call itself are in the module _native (csrc/binding.cpp).
 
 Q8_BLOCK = 64                                   # slots that share a scale
 _Q8_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
 _Q8_DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+_binding = None
+
+
+def _load_binding():
+    """The module that takes tensors to the library's calls; like the library, it must have been built."""
+    global _binding
+    lib = load_library()
+    try:
+        from . import _native as module
+    except ImportError as e:
+        raise ImportError(f"{_HERE}/_native.so cannot be loaded ({e}): build it with "
+                          "`python -m sliding_window_gqa_chunk_b200.csrc.build`") from e
+    calls = (lib.swa_q8_append, lib.swa_q8_prefill_chunk, lib.swa_q8_decode, lib.swa_rope)
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in calls))
+    _binding = module
+    return module
 
 
 def _arg(name: str, t: torch.Tensor, shape, dtype: torch.dtype, dev: int) -> int:
@@ -322,26 +357,11 @@ def _device_of(name: str, t: torch.Tensor) -> int:
     return t.get_device()
 
 
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _run(dev: int, stream, name: str, *args) -> None:
-    """The library's call `name` with dev current (where the tensors are), on `stream` or dev's current one."""
-    if stream is None:
-        stream = _current_stream(dev)
-    else:
-        if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
-            raise ValueError(f"stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
-        stream = _stream(stream)
-    fn = getattr(_lib or load_library(), name)
-    if _current_device() == dev:
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream)
-    if rc != SWA_OK:
-        _check(rc)
+def _handle(stream, dev: int) -> int:
+    """A stream's handle (a torch stream of another device is refused)."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
+    return _stream(stream).value or 0
 
 
 @dataclasses.dataclass(frozen=True, eq=False)
@@ -373,15 +393,12 @@ class CacheQ8:
                 _arg("v_scale", self.v_scale, blocks, torch.float32, dev),
                 _arg("k_tail", self.k_tail, tail, torch.bfloat16, dev),
                 _arg("v_tail", self.v_tail, tail, torch.bfloat16, dev)]
-        object.__setattr__(self, "_ref", ctypes.byref(_CCacheQ8(*ptrs, _Q8_FORMATS[self.k.dtype])))
-        object.__setattr__(self, "_dev", dev)
-        object.__setattr__(self, "_shape", (B, H, W, d))
+        record = _CacheRecord(_CCacheQ8(*ptrs, _Q8_FORMATS[self.k.dtype]), B, H, W, d, dev)
+        object.__setattr__(self, "_record", record)
+        object.__setattr__(self, "_cache_addr", ctypes.addressof(record))
 
-    def _for(self, dims: Dims) -> int:
-        """The device of the cache, once it is known to be one of these dims."""
-        if self._shape != (dims.batch, dims.n_kv_heads, dims.window, dims.head_dim):
-            raise ValueError(f"cache of [B, Hkv, W, d] = {self._shape} for {dims}")
-        return self._dev
+    def __reduce__(self):       # a copy makes its own record
+        return CacheQ8, (self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
 
 
 def new_cache_q8(dims: Dims, format: str = "e4m3", device="cuda") -> CacheQ8:
@@ -403,16 +420,15 @@ def new_cache_q8(dims: Dims, format: str = "e4m3", device="cuda") -> CacheQ8:
 def cache_append_q8(dims: Dims, cache: CacheQ8, k, v, start_pos, n_tokens, stream=None) -> None:
     """swa_q8_append: k/v [B, T, Hkv, d] bf16 into the 8-bit cache, blocks that they fill up
     rounded, the rest in the tail."""
-    dev = cache._for(dims)
-    B, T = dims.batch, k.shape[1]
-    rows = (B, T, dims.n_kv_heads, dims.head_dim)
-    _run(dev, stream, "swa_q8_append", dims._ref, cache._ref, _arg("k", k, rows, torch.bfloat16, dev),
-         _arg("v", v, rows, torch.bfloat16, dev), T, _arg("start_pos", start_pos, (B,), torch.int32, dev),
-         _arg("n_tokens", n_tokens, (B,), torch.int32, dev))
+    if stream is not None:
+        stream = _handle(stream, cache._record.device)
+    rc = (_binding or _load_binding()).append(dims, cache, k, v, start_pos, n_tokens, stream)
+    if rc:
+        _check(rc)
 
 
 def prefill_workspace_size_q8(dims: Dims, max_tokens: int) -> int:
-    return int(load_library().swa_q8_prefill_workspace_size(dims._ref, int(max_tokens)))
+    return int(load_library().swa_q8_prefill_workspace_size(ctypes.byref(dims._record), int(max_tokens)))
 
 
 def prefill_workspace_q8(dims: Dims, max_tokens: int, device="cuda") -> torch.Tensor:
@@ -423,18 +439,15 @@ def prefill_workspace_q8(dims: Dims, max_tokens: int, device="cuda") -> torch.Te
 def prefill_chunk_q8(dims: Dims, out, q, k, v, cache: CacheQ8, start_pos, n_tokens, workspace,
                      stream=None) -> None:
     """swa_q8_prefill_chunk: out [B, T, Hq, d] = attention of chunk q over (8-bit cache + chunk k/v)."""
-    dev = cache._for(dims)
-    B, T = dims.batch, q.shape[1]
-    heads, rows = (B, T, dims.n_q_heads, dims.head_dim), (B, T, dims.n_kv_heads, dims.head_dim)
-    _run(dev, stream, "swa_q8_prefill_chunk", dims._ref, _arg("out", out, heads, dims.torch_out_dtype, dev),
-         _arg("q", q, heads, torch.bfloat16, dev), _arg("k", k, rows, torch.bfloat16, dev),
-         _arg("v", v, rows, torch.bfloat16, dev), T, cache._ref, _arg("start_pos", start_pos, (B,), torch.int32, dev),
-         _arg("n_tokens", n_tokens, (B,), torch.int32, dev),
-         _arg("workspace", workspace, workspace.shape, workspace.dtype, dev), workspace.nbytes)
+    if stream is not None:
+        stream = _handle(stream, cache._record.device)
+    rc = (_binding or _load_binding()).prefill(dims, out, q, k, v, cache, start_pos, n_tokens, workspace, stream)
+    if rc:
+        _check(rc)
 
 
 def decode_workspace_size_q8(dims: Dims) -> int:
-    return int(load_library().swa_q8_decode_workspace_size(dims._ref))
+    return int(load_library().swa_q8_decode_workspace_size(ctypes.byref(dims._record)))
 
 
 def decode_workspace_q8(dims: Dims, device="cuda") -> torch.Tensor:
@@ -444,13 +457,11 @@ def decode_workspace_q8(dims: Dims, device="cuda") -> torch.Tensor:
 
 def decode_q8(dims: Dims, out, q, k_new, v_new, cache: CacheQ8, pos, workspace, stream=None) -> None:
     """swa_q8_decode: take (k_new, v_new) in at position pos, then out [B, Hq, d] = attention."""
-    dev = cache._for(dims)
-    B, d = dims.batch, dims.head_dim
-    heads, rows = (B, dims.n_q_heads, d), (B, dims.n_kv_heads, d)
-    _run(dev, stream, "swa_q8_decode", dims._ref, _arg("out", out, heads, dims.torch_out_dtype, dev),
-         _arg("q", q, heads, torch.bfloat16, dev), _arg("k_new", k_new, rows, torch.bfloat16, dev),
-         _arg("v_new", v_new, rows, torch.bfloat16, dev), cache._ref, _arg("pos", pos, (B,), torch.int32, dev),
-         _arg("workspace", workspace, workspace.shape, workspace.dtype, dev), workspace.nbytes)
+    if stream is not None:
+        stream = _handle(stream, cache._record.device)
+    rc = (_binding or _load_binding()).decode(dims, out, q, k_new, v_new, cache, pos, workspace, stream)
+    if rc:
+        _check(rc)
 
 
 @dataclasses.dataclass(frozen=True, eq=False)
@@ -467,8 +478,12 @@ class Rope:
         dev = _device_of("inv_freq", self.inv_freq)
         n = self.inv_freq.numel()
         ptr = _arg("inv_freq", self.inv_freq, (n,), torch.float32, dev)
-        object.__setattr__(self, "_ref", ctypes.byref(_CRope(ptr, 2 * n, int(self.interleaved), float(self.factor))))
-        object.__setattr__(self, "_dev", dev)
+        record = _RopeRecord(_CRope(ptr, 2 * n, int(self.interleaved), float(self.factor)), dev)
+        object.__setattr__(self, "_record", record)
+        object.__setattr__(self, "_rope_addr", ctypes.addressof(record))
+
+    def __reduce__(self):       # a copy makes its own record
+        return Rope, (self.inv_freq, self.interleaved, self.factor)
 
 
 def new_rope(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
@@ -501,36 +516,14 @@ def new_rope(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, 
     return Rope(freq.float().to(device), interleaved, factor)
 
 
-def _rows(name: str, t: torch.Tensor, shape, dev: int):
-    """(address, elements from row to row) of q or k [B, T, H, d], heads dense, rows evenly spaced."""
-    B, T, H, d = shape
-    if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev:
-        if t.is_contiguous():
-            return t.data_ptr(), H * d
-        s = t.stride()
-        row = s[1] if T > 1 else s[0] if B > 1 else H * d
-        if s[3] == 1 and (H == 1 or s[2] == d) and (B == 1 or s[0] == T * row):
-            return t.data_ptr(), row
-    raise ValueError(f"{name}: expected a bfloat16 tensor of shape {tuple(shape)} on cuda:{dev} with dense heads and "
-                     f"evenly spaced rows, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
 def rope(dims: Dims, spec: Rope, q_out, k_out, q, k, start_pos, n_tokens=None, transpose: bool = False,
          stream=None) -> None:
     """swa_rope: q [B, T, Hq, d] and k [B, T, Hkv, d] (bf16; heads inside a packed projection are
     taken as they lie) turned to positions start_pos[b] + t, into dense q_out and k_out (which may be
     q and k if those are dense).  k and k_out may be None.  ``n_tokens`` None: all T rows.
     ``transpose`` gives the gradient for q and k from that for q_out and k_out."""
-    dev = spec._dev
-    B, T, d = dims.batch, q.shape[1], dims.head_dim
-    heads, rows = (B, T, dims.n_q_heads, d), (B, T, dims.n_kv_heads, d)
-    qp, qs = _rows("q", q, heads, dev)
-    qo, kp, ks, ko = _arg("q_out", q_out, heads, torch.bfloat16, dev), None, 0, None
-    if k is not None or k_out is not None:
-        if k is None or k_out is None:
-            raise ValueError("k and k_out: both or neither")
-        kp, ks = _rows("k", k, rows, dev)
-        ko = _arg("k_out", k_out, rows, torch.bfloat16, dev)
-    _run(dev, stream, "swa_rope", dims._ref, spec._ref, qo, ko, qp, kp, qs, ks, T,
-         _arg("start_pos", start_pos, (B,), torch.int32, dev),
-         None if n_tokens is None else _arg("n_tokens", n_tokens, (B,), torch.int32, dev), 1 if transpose else 0)
+    if stream is not None:
+        stream = _handle(stream, spec._record.device)
+    rc = (_binding or _load_binding()).rope(dims, spec, q_out, k_out, q, k, start_pos, n_tokens, transpose, stream)
+    if rc:
+        _check(rc)

@@ -234,3 +234,15 @@ def test_frequencies_of_the_scaled_forms(monkeypatch):
     np.testing.assert_allclose(f[turns > 32], plain[turns > 32], rtol=2.0 ** -22)
     np.testing.assert_allclose(f[turns < 1], plain[turns < 1] / 4, rtol=2.0 ** -22)
     assert (turns > 32).any() and (turns < 1).any() and abs(c - (0.1 * math.log(4) + 1)) < 1e-12
+
+
+def test_dims_copies_make_their_own_records():
+    """The address that the binding module reads belongs to one object: copies and pickles do not take it along."""
+    import copy
+    import pickle
+
+    d = swa.Dims(1, 2, 1, 16, 64, 0.25)
+    first = d._dims_addr
+    for e in (copy.copy(d), copy.deepcopy(d), pickle.loads(pickle.dumps(d))):
+        assert e == d and "_record" not in e.__dict__ and e._dims_addr != first
+    assert d._dims_addr == first and hash(d) == hash(swa.Dims(1, 2, 1, 16, 64, 0.25))
