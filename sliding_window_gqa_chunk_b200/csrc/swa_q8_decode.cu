@@ -173,16 +173,14 @@ __device__ __forceinline__ int f16_exp(uint32_t amax) {
   return e < -126 ? -126 : (e > 113 ? 113 : e);
 }
 
-template <int D>
-constexpr int q8_o_stride() { return D + 1; }
 // Shared memory of the merge: m, l and O of each warp (in the rings, once every warp is
 // done with its own), and what the CTAs of a cluster send to one another.
 template <int D, int NT, int NW>
 constexpr int q8_merge_bytes() {
-  return (int)sizeof(float) * NW * 8 * NT * (2 + q8_o_stride<D>());
+  return (int)sizeof(float) * NW * 8 * NT * (2 + D);
 }
 template <int D, int NT>
-constexpr int q8_peer_floats() { return kMaxCluster * 8 * NT * 2 + 8 * NT * D + kMaxCluster; }
+constexpr int q8_peer_floats() { return kMaxCluster * 8 * NT * 2 + 8 * NT * D + 4 * kMaxCluster; }
 template <int D, int NT, int NW, int R>
 constexpr int q8_ring_bytes() {
   constexpr int ring = NW * R * kTileRows * D, merge = q8_merge_bytes<D, NT, NW>();
@@ -199,10 +197,26 @@ constexpr int q8_smem_bytes() {
 __device__ __forceinline__ void cluster_begun_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
 __device__ __forceinline__ void cluster_begun_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void store_out(void* out, size_t i, float x, int f32) {
-  if (f32) reinterpret_cast<float*>(out)[i] = x;
-  else reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
-}
+// Four elements of an output: sums against a maximum m.
+struct Four {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ Four() : m(-INFINITY), l(0.f), o(make_float4(0.f, 0.f, 0.f, 0.f)) {}
+  __device__ __forceinline__ void add(float s, float l2, const float4& o2) {
+    l += s * l2;
+    o.x += s * o2.x;
+    o.y += s * o2.y;
+    o.z += s * o2.z;
+    o.w += s * o2.w;
+  }
+  // the i-th four of the output; weights are in units of kWeightUnit, their sum is not
+  __device__ __forceinline__ void store(void* out, size_t i, int f32) const {
+    const float x = o.x * kWeightUnit / l, y = o.y * kWeightUnit / l;
+    const float z = o.z * kWeightUnit / l, w = o.w * kWeightUnit / l;
+    if (f32) reinterpret_cast<float4*>(out)[i] = make_float4(x, y, z, w);
+    else reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
+  }
+};
 
 // Running softmax state of one n-tile (8 heads) of a warp: lane (g, t) holds
 // heads 2t and 2t + 1; O rows (mt, g) and (mt, g + 8) are elements
@@ -331,6 +345,9 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       qf[nt][2 * w + 1] = x.y;
     }
   }
+  uint4 fresh = make_uint4(0, 0, 0, 0);              // the new row, for the tail
+  if (!CHUNK && warp == NW - 1 && lane < 2 * (D / 8))
+    fresh = ldg_stream(reinterpret_cast<const uint4*>((lane < D / 8 ? p.k_new : p.v_new) + unit * D) + lane % (D / 8));
   const long long pos = p.pos[b];
   const int n_rows = CHUNK ? p.n_tokens[b] : 1;
   if (pos < 0 || n_rows < 0 || (CHUNK && n_rows > p.max_tokens)) {
@@ -358,6 +375,14 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   const __nv_bfloat16* kn = p.k_new + (CHUNK ? ((size_t)b * p.max_tokens * p.n_kv_heads + kvh) : unit) * D;
   const __nv_bfloat16* vn = p.v_new + (CHUNK ? ((size_t)b * p.max_tokens * p.n_kv_heads + kvh) : unit) * D;
   const size_t new_stride = (size_t)p.n_kv_heads * D;
+
+  // The new row goes in: into the tail now (no one reads that row there), or, if it fills its block up,
+  // with the tail into the ring when this CTA, the only one to read the tail, is done.
+  const bool fills = !CHUNK && owner && s_new + 1 == min(blk0 + kQ8Block, W);
+  if (!CHUNK && owner && !fills && warp == NW - 1 && lane < 2 * (D / 8)) {
+    const int i = lane % (D / 8);
+    reinterpret_cast<uint4*>((lane < D / 8 ? kt : vt) + (size_t)row_new * D)[i] = fresh;
+  }
 
   // The warp's blocks: those of its split in turn.  Rows [first_row(x), r_end) of the block at
   // slot x are held in 8 bits and in the window; the block being filled may have none.
@@ -681,17 +706,16 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
 
   // ---- merge the NW warps of the CTA ----
-  // in the rings, once every warp is done with its own: m[NW][G8], l[NW][G8], O[NW][G8][kOS]
+  // in the rings, once every warp is done with its own: (m, l)[NW][G8], then O[NW][G8][D] with the
+  // c-th four of a column h at c ^ (h / 2 & 3), so that the four columns of a store fall on different banks
   __syncthreads();
-  constexpr int G8 = 8 * NT;
-  constexpr int kOS = q8_o_stride<D>();
-  float* sm_m = smem;
-  float* sm_l = sm_m + NW * G8;
-  float* sm_o = sm_l + NW * G8;
+  constexpr int G8 = 8 * NT, D4 = D / 4;
+  float2* sm_ml = reinterpret_cast<float2*>(smem_al);
+  float4* sm_o = reinterpret_cast<float4*>(sm_ml + NW * G8);
   uint32_t* red = reinterpret_cast<uint32_t*>(smem_al + q8_ring_bytes<D, NT, NW, R>());
-  // what the peers of a cluster send: (m, l)[rank][G8] and O[rank][share]
-  float* peer_ml = reinterpret_cast<float*>(smem_al + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8);
-  float* peer_o = peer_ml + kMaxCluster * G8 * 2;
+  // what the peers of a cluster send: O[rank][share], then (m, l)[rank][G8]
+  float4* peer_o = reinterpret_cast<float4*>(smem_al + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8);
+  float2* peer_ml = reinterpret_cast<float2*>(peer_o + G8 * D4 + kMaxCluster);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float l0 = st[nt].l[0], l1 = st[nt].l[1];
@@ -700,21 +724,19 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
-    const int h0 = nt * 8 + 2 * t;
-    if (g == 0) {
-      sm_m[warp * G8 + h0] = st[nt].m[0];
-      sm_m[warp * G8 + h0 + 1] = st[nt].m[1];
-      sm_l[warp * G8 + h0] = l0;
-      sm_l[warp * G8 + h0 + 1] = l1;
-    }
-    float* oh0 = sm_o + ((size_t)warp * G8 + h0) * kOS + g * (D / 8);
-    float* oh1 = oh0 + kOS;
 #pragma unroll
-    for (int mt = 0; mt < F::kMTiles; ++mt) {
-      oh0[2 * mt] = st[nt].o[mt][0];
-      oh1[2 * mt] = st[nt].o[mt][1];
-      oh0[2 * mt + 1] = st[nt].o[mt][2];
-      oh1[2 * mt + 1] = st[nt].o[mt][3];
+    for (int e = 0; e < 2; ++e) {
+      const int h = nt * 8 + 2 * t + e;
+      if (g == 0) sm_ml[warp * G8 + h] = make_float2(st[nt].m[e], e ? l1 : l0);
+      float4* o = sm_o + (warp * G8 + h) * D4;
+      if constexpr (D == 16) {                 // two elements a lane
+        reinterpret_cast<float2*>(o)[2 * ((g / 2) ^ t) + (g & 1)] = make_float2(st[nt].o[0][e], st[nt].o[0][2 + e]);
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < F::kMTiles; mt += 2)
+          o[(g * (D / 32) + mt / 2) ^ t] =
+              make_float4(st[nt].o[mt][e], st[nt].o[mt][2 + e], st[nt].o[mt + 1][e], st[nt].o[mt + 1][2 + e]);
+      }
     }
   }
   __syncthreads();
@@ -723,96 +745,76 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   const int n_cl = p.cluster ? p.n_splits : 1, rank = p.cluster ? split : 0;
-  const int per = (cols * D + n_cl - 1) / n_cl;      // outputs that a CTA of the cluster merges
+  const int per = (cols * D4 + n_cl - 1) / n_cl;     // fours that a CTA of the cluster merges
   const int live = CHUNK ? min(cols, n_rows * G - c0) : cols;   // columns with a row
-  for (int idx = threadIdx.x; idx < cols * D; idx += NW * 32) {
-    const int h = idx / D, dd = idx % D;
-    float M = -CUDART_INF_F;
+  for (int idx = threadIdx.x; idx < cols * D4; idx += NW * 32) {
+    const int h = idx / D4, c = idx % D4;
+    Four f;
+    float2 ml[NW];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w * G8 + h]);
-    float L = 0.f, O = 0.f;
-    if (M != -CUDART_INF_F) {
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float sc = fast_exp2(sm_m[w * G8 + h] - M);
-        L += sc * sm_l[w * G8 + h];
-        O += sc * sm_o[((size_t)w * G8 + h) * kOS + dd];
-      }
+    for (int w = 0; w < NW; ++w) {
+      ml[w] = sm_ml[w * G8 + h];
+      f.m = fmaxf(f.m, ml[w].x);
     }
-    const size_t bh = row_of(h);
+    if (f.m != -CUDART_INF_F) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        f.add(fast_exp2(ml[w].x - f.m), ml[w].y, sm_o[(w * G8 + h) * D4 + (c ^ (h / 2 & 3))]);
+    }
     if (p.n_splits == 1) {
-      if (h < live) store_out(p.out, bh * D + dd, O * kWeightUnit / L, p.out_f32);
+      if (h < live) f.store(p.out, row_of(h) * D4 + c, p.out_f32);
     } else if (CHUNK || p.cluster) {
-      // each output to the CTA that merges it, m and l to all
-      cl.map_shared_rank(peer_o, idx / per)[rank * per + idx % per] = O;
-      if (dd < n_cl)
-        reinterpret_cast<float2*>(cl.map_shared_rank(peer_ml, dd))[rank * G8 + h] = make_float2(M, L);
+      // each four to the CTA that merges it, m and l to all
+      cl.map_shared_rank(peer_o, idx / per)[rank * per + idx % per] = f.o;
+      for (int r = c; r < n_cl; r += D4) cl.map_shared_rank(peer_ml, r)[rank * G8 + h] = make_float2(f.m, f.l);
     } else {
-      p.ws_o[(bh * p.n_splits + split) * D + dd] = O;
-      if (dd == 0) {
-        p.ws_ml[(bh * p.n_splits + split) * 2] = M;
-        p.ws_ml[(bh * p.n_splits + split) * 2 + 1] = L;
-      }
+      const size_t part = row_of(h) * p.n_splits + split;
+      reinterpret_cast<float4*>(p.ws_o)[part * D4 + c] = f.o;
+      if (c == 0) reinterpret_cast<float2*>(p.ws_ml)[part] = make_float2(f.m, f.l);
     }
   }
 
   if (p.cluster) {
     cl.sync();   // all has been sent; every CTA of the pair's cluster comes here
-    for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < live * D; idx += NW * 32) {
-      const int h = idx / D;
-      float M = -CUDART_INF_F;
-      for (int r = 0; r < n_cl; ++r) M = fmaxf(M, reinterpret_cast<float2*>(peer_ml)[r * G8 + h].x);
-      float L = 0.f, O = 0.f;
+    for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < live * D4; idx += NW * 32) {
+      const int h = idx / D4;
+      Four f;
+      for (int r = 0; r < n_cl; ++r) f.m = fmaxf(f.m, peer_ml[r * G8 + h].x);
       for (int r = 0; r < n_cl; ++r) {
-        const float2 ml = reinterpret_cast<float2*>(peer_ml)[r * G8 + h];
-        const float sc = ml.x == -CUDART_INF_F ? 0.f : fast_exp2(ml.x - M);
-        L += sc * ml.y;
-        O += sc * peer_o[r * per + idx - rank * per];
+        const float2 ml = peer_ml[r * G8 + h];
+        f.add(fast_exp2(ml.x - f.m), ml.y, peer_o[r * per + idx - rank * per]);
       }
-      store_out(p.out, row_of(h) * D + idx % D, O * kWeightUnit / L, p.out_f32);
+      f.store(p.out, row_of(h) * D4 + idx % D4, p.out_f32);
     }
   }
 
-  if (!CHUNK && owner) {
-    const int size = min(kQ8Block, W - blk0);
-    if (row_new + 1 == size) {
-      auto k_row = [&](int i) { return i == row_new ? kn : kt + (size_t)i * D; };
-      auto v_row = [&](int i) { return i == row_new ? vn : vt + (size_t)i * D; };
-      const size_t dst = (unit * W + blk0) * D;
-      q8::round_block<D, FMT, NW * 32>(k_row, v_row, size, p.ring.k8 + dst, p.ring.v8 + dst,
-                              p.ring.k_scale + unit * n_blocks + blk0 / kQ8Block,
-                              p.ring.v_scale + unit * n_blocks + blk0 / kQ8Block, red);
-    } else if (warp == 0) {
-      for (int i = lane; i < D / 8; i += 32) {
-        reinterpret_cast<uint4*>(kt + (size_t)row_new * D)[i] = reinterpret_cast<const uint4*>(kn)[i];
-        reinterpret_cast<uint4*>(vt + (size_t)row_new * D)[i] = reinterpret_cast<const uint4*>(vn)[i];
-      }
-    }
+  if (fills) {
+    auto k_row = [&](int i) { return i == row_new ? kn : kt + (size_t)i * D; };
+    auto v_row = [&](int i) { return i == row_new ? vn : vt + (size_t)i * D; };
+    const size_t dst = (unit * W + blk0) * D;
+    q8::round_block<D, FMT, NW * 32>(k_row, v_row, row_new + 1, p.ring.k8 + dst, p.ring.v8 + dst,
+                                     p.ring.k_scale + unit * n_blocks + blk0 / kQ8Block,
+                                     p.ring.v_scale + unit * n_blocks + blk0 / kQ8Block, red);
   }
 }
 
-// Merge of the per-split partials: grid B * Hq, one thread per element.
+// Merge of the per-split partials: grid B * Hq, a thread to four elements.
 template <int D>
-__global__ void __launch_bounds__(D < 32 ? 32 : D) swa_q8_decode_combine_kernel(const Q8DecodeParams p) {
+__global__ void __launch_bounds__(32) swa_q8_decode_combine_kernel(const Q8DecodeParams p) {
   wait_prior_grid();
   allow_next_grid();
   const size_t bh = blockIdx.x;
-  const int dd = threadIdx.x;
-  if (dd >= D || p.pos[bh / p.n_q_heads] < 0) return;
+  const int c = threadIdx.x;
+  if (c >= D / 4 || p.pos[bh / p.n_q_heads] < 0) return;
   const int S = p.n_splits;
-  const float* ml = p.ws_ml + bh * S * 2;
-  float M = -CUDART_INF_F;
-  for (int s = 0; s < S; ++s) M = fmaxf(M, ml[2 * s]);
-  float L = 0.f, O = 0.f;
-  const float* op = p.ws_o + bh * S * D + dd;
-  for (int s = 0; s < S; ++s) {
-    const float m = ml[2 * s];
-    if (m == -CUDART_INF_F) continue;
-    const float sc = fast_exp2(m - M);
-    L += sc * ml[2 * s + 1];
-    O += sc * op[(size_t)s * D];
-  }
-  store_out(p.out, bh * D + dd, O * kWeightUnit / L, p.out_f32);
+  const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + bh * S;
+  const float4* o = reinterpret_cast<const float4*>(p.ws_o) + bh * S * (D / 4) + c;
+  Four f;
+#pragma unroll 8
+  for (int s = 0; s < S; ++s) f.m = fmaxf(f.m, ml[s].x);
+#pragma unroll 8
+  for (int s = 0; s < S; ++s) f.add(fast_exp2(ml[s].x - f.m), ml[s].y, o[(size_t)s * (D / 4)]);
+  f.store(p.out, bh * (D / 4) + c, p.out_f32);
 }
 
 namespace {
@@ -854,7 +856,7 @@ cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStre
   if (e != cudaSuccess || p.n_splits == 1 || p.cluster) return e;
   cudaLaunchConfig_t ccfg = {};
   ccfg.gridDim = dim3((unsigned)((size_t)p.batch * p.n_q_heads));
-  ccfg.blockDim = dim3(D < 32 ? 32 : D);
+  ccfg.blockDim = dim3(32);
   ccfg.stream = stream;
   ccfg.attrs = attr;
   ccfg.numAttrs = 1;
