@@ -24,7 +24,8 @@ LIB = os.path.join(PKG, "libswa.so")
 BINDING = os.path.join(PKG, "_native.so")
 
 SOURCES = ["swa_api.cu", "swa_append.cu", "swa_decode.cu", "swa_prefill.cu", "swa_decode_static.cu",
-           "swa_q8_api.cu", "swa_q8_cache.cu", "swa_q8_decode.cu", "swa_rope.cu"]
+           "swa_q8_api.cu", "swa_q8_cache.cu", "swa_q8_decode.cu", "swa_q8_decode_16.cu",
+           "swa_q8_decode_64.cu", "swa_q8_decode_128.cu", "swa_rope.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -169,26 +169,33 @@ struct Q8DecodeParams {
   int max_tokens, groups;       // rows of a chunk, CTAs that share its columns
   int batch, n_q_heads, n_kv_heads, head_dim, window;
   int n_splits, slots_per_split;
-  int warps;                    // warps per CTA
+  int variant;                  // of kQ8Variants
   int cluster;                  // 1: the splits of a pair merge in a thread-block cluster
   float scale_log2;             // scale * log2(e)
   int out_f32;
 };
+// CTAs of the q8 decode kernel: warps, tiles in each warp's ring, CTAs an SM holds.
+struct Q8Variant {
+  int warps, tiles, per_sm;
+};
+constexpr Q8Variant kQ8Variants[3] = {{8, 6, 1}, {4, 6, 2}, {4, 4, 3}};
+constexpr int kQ8TileRows = 32;        // rows of a tile
+constexpr int kQ8MaxCluster = 8;       // portable cluster size
+constexpr int kQ8FewColumns = 128;     // of a chunk that goes over the ring's bytes
 // Split of the W slots of one (sequence, kv head); a function of the shape.
 struct Q8DecodeSplit {
-  int n_splits, slots_per_split, warps, cluster;
+  int n_splits, slots_per_split, variant, cluster;
 };
-Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int groups, bool chunk);
+Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int head_dim, int groups, bool chunk, bool wide);
 // Chunks of at most this many columns (rows x query heads of a kv head) go through launch_q8_decode
 // too, with q, k, v and out as in the prefill and start positions as pos.
 int q8_few_columns();
 int q8_chunk_groups(int columns);
 // TMA descriptors of the ring's keys and values: [B * Hkv][W][d] bytes, boxes of
-// q8_decode_box_rows() rows, swizzled by the row's size.
+// kQ8TileRows rows, swizzled by the row's size.
 struct Q8DecodeMaps {
   CUtensorMap k, v;
 };
-int q8_decode_box_rows();
 cudaError_t launch_q8_decode(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream);
 
 struct RopeParams {

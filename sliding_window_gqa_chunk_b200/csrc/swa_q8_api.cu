@@ -65,6 +65,11 @@ size_t ring_bytes(const swa_dims* dims) {   // of the keys or of the values
   return (size_t)dims->batch * dims->n_kv_heads * dims->window * dims->head_dim * sizeof(__nv_bfloat16);
 }
 
+swa::Q8DecodeSplit split_of(const swa_dims* dims, int groups, bool chunk) {
+  return swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, dims->head_dim, groups, chunk,
+                              dims->n_q_heads / dims->n_kv_heads > 8);
+}
+
 // Fills in what decode steps and short chunks share, and launches.
 int launch_over_ring(swa::Q8DecodeParams& p, const swa_dims* dims, const swa_q8_cache* cache, void* out, const void* q,
                      const void* k, const void* v, const int32_t* pos, const swa::Q8DecodeSplit& sp, void* stream,
@@ -81,7 +86,7 @@ int launch_over_ring(swa::Q8DecodeParams& p, const swa_dims* dims, const swa_q8_
   p.window = dims->window;
   p.n_splits = sp.n_splits;
   p.slots_per_split = sp.slots_per_split;
-  p.warps = sp.warps;
+  p.variant = sp.variant;
   p.cluster = sp.cluster;
   p.scale_log2 = dims->scale * 1.4426950408889634f;
   p.out_f32 = dims->out_dtype == SWA_DTYPE_F32;
@@ -89,9 +94,8 @@ int launch_over_ring(swa::Q8DecodeParams& p, const swa_dims* dims, const swa_q8_
   if (rc) return rc;
   swa::Q8DecodeMaps maps;
   const long long pairs = (long long)dims->batch * dims->n_kv_heads;
-  const int box = swa::q8_decode_box_rows();
-  if ((rc = swa::api_encode_bytes(&maps.k, cache->k, dims->head_dim, dims->window, pairs, box, "cache k"))) return rc;
-  if ((rc = swa::api_encode_bytes(&maps.v, cache->v, dims->head_dim, dims->window, pairs, box, "cache v"))) return rc;
+  if ((rc = swa::api_encode_bytes(&maps.k, cache->k, dims->head_dim, dims->window, pairs, swa::kQ8TileRows, "cache k"))) return rc;
+  if ((rc = swa::api_encode_bytes(&maps.v, cache->v, dims->head_dim, dims->window, pairs, swa::kQ8TileRows, "cache v"))) return rc;
   const cudaError_t e = swa::launch_q8_decode(p, maps, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, what);
   return swa::api_ok();
@@ -156,7 +160,7 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
     d.n_tokens = n_tokens;
     d.max_tokens = max_tokens;
     d.groups = groups;
-    const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, d.groups, true);
+    const swa::Q8DecodeSplit sp = split_of(dims, d.groups, true);
     return launch_over_ring(d, dims, cache, out, q, k, v, start_pos, sp, stream, "swa_q8_prefill_chunk");
   }
   // the prefill's own limit, before the ring is expanded: a refused call enqueues nothing
@@ -183,7 +187,7 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
 
 size_t swa_q8_decode_workspace_size(const swa_dims* dims) {
   if (check_q8_dims(dims) != SWA_OK) return 0;
-  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1, false);
+  const swa::Q8DecodeSplit sp = split_of(dims, 1, false);
   if (sp.n_splits == 1 || sp.cluster) return 16;  // nothing needed; a non-zero size keeps callers simple
   return (size_t)dims->batch * dims->n_q_heads * sp.n_splits * (dims->head_dim + 2) * sizeof(float);
 }
@@ -202,7 +206,7 @@ int swa_q8_decode(const swa_dims* dims, void* out, const void* q, const void* k_
   if (workspace_bytes < need)
     return swa::api_fail(SWA_ERR_WORKSPACE_TOO_SMALL, "q8 decode workspace of %zu bytes, %zu needed",
                          workspace_bytes, need);
-  const swa::Q8DecodeSplit sp = swa::q8_decode_split(dims->batch, dims->n_kv_heads, dims->window, 1, false);
+  const swa::Q8DecodeSplit sp = split_of(dims, 1, false);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = p.ws_o + (size_t)dims->batch * dims->n_q_heads * sp.n_splits * dims->head_dim;
   p.n_tokens = nullptr;

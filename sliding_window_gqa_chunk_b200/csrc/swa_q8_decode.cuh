@@ -1,0 +1,895 @@
+// swa_q8_decode.cuh - attention of one token, or of a chunk's few rows, over the 8-bit
+// rolling cache.
+//
+// A decode step attends over the min(pos + 1, W) positions (pos - W, pos], as the
+// bf16 one does, over half the bytes: every (sequence, kv head) streams W slots x
+// d x 1 B of keys and the same of values.  One warp handles all G query heads of its
+// kv head, and the dot products run on mma.sync m16n8k16 in f16 with fp32 sums, in
+// which every 8-bit number is exact:
+//
+//   S^T[slot][head] = K[slot][:] . Q[head][:]        (M = 16 slots, N = 8 heads, K = d)
+//   O^T[d][head]   += V^T[d][slot] . P^T[slot][head] (M = 16 d, N = 8 heads, K = 16 slots)
+//
+// tcgen05 has nothing to offer here: at G = 4 the tensor pipe is busy for a fifth of
+// the time that the bytes take, and its operands would have to be written back to
+// shared memory in 16 bits.
+//
+// Scales.  A block's key scale multiplies its scores.  Its value scale 2^v is put into
+// the exponent of the softmax: with x the score in log2 units, the weight of a slot is
+// w = 2^(x + v - m + 15), where the running m is the maximum of x + v rather than of x.
+// The numbers of a block's values always reach the top of their format, so w orders the
+// slots by what they can add to the output and is at most 2^15: f16 keeps 11 bits of the
+// weights down to 2^-29 of the largest.  The softmax sum is that of 2^(x - m) =
+// w 2^(-v - 15), in fp32.  Q goes to f16 with one power of two for each head (its largest
+// magnitude to [2^14, 2^15)): its 8 bits are kept in all elements above 2^-28 of the
+// largest.  The rows of the block being filled (at most 64, in bf16) go through the same
+// products, 16 rows with a power of two of their own at a time.
+//
+// Bytes.  The bound is HBM: 538 MB for 64 sequences of W = 4096 with 8 kv heads of 128
+// take 88 us (6.1 TB/s of 6.56 measured for a copy).  Each warp streams its blocks through
+// a ring of its own in shared memory, 6 tiles of 32 rows, filled by TMA and freed by the
+// warp when the tile is in registers; no warp waits for another before the merge.  8 warps
+// an SM keep 192 KB in flight.  Loads into registers with 12 warps an SM took 172 us; rings of
+// 12 KB for 16 warps 100 us (the arithmetic of a block is as long as a ring).
+//
+// Work split: grid (n_splits, Hkv, B); the warps of a CTA take the 64-slot blocks of its split
+// in turn and merge their (m, l, O) in shared memory, and the splits of a pair merge through
+// distributed shared memory (thread-block cluster) or through the workspace and a second
+// kernel.  The CTA whose split holds slot pos mod W takes the rows of the tail into its sweep,
+// writes the new row there or, if it is its block's last, rounds the block into the ring.  That
+// block's old rows are then all out of the window, so no CTA reads what is being written.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "swa_common.cuh"
+#include "swa_internal.h"
+#include "swa_q8.cuh"
+#include "swa_tc.cuh"
+
+namespace swa {
+
+namespace {
+
+constexpr int kSub = 16;            // slots of one mma block
+constexpr int kSubs = kQ8Block / kSub;        // mma blocks of a scale block
+constexpr int kTileRows = kQ8TileRows;        // rows of a TMA tile
+constexpr int kTileSubs = kTileRows / kSub;
+constexpr int kTiles = kQ8Block / kTileRows;  // tiles of a block's keys (and of its values)
+constexpr int kMaxCluster = kQ8MaxCluster;
+constexpr float kWeightExp = 15.f;  // the largest weight is 2^15
+constexpr float kWeightUnit = 1.f / 32768.f;
+constexpr int kChunkRows = kQ8FewColumns;     // a chunk of so many columns has at most as many rows
+
+// Row fragments of a lane: bytes of a key row (D / 4) and of a value row (D / 8).
+template <int D>
+struct Q8Frag {
+  static constexpr int kKWords = D / 16;                    // 4 numbers each = one mma k-step
+  static constexpr int kVBytes = D / 8;
+  static constexpr int kVWords = kVBytes < 4 ? 1 : kVBytes / 4;
+  static constexpr int kMTiles = D / 16;
+};
+
+// Tiles in shared memory lie as TMA writes them: rows of D bytes whose 16-byte
+// pieces are permuted (128-byte swizzle for d = 128: piece ^ (row & 7), 64-byte
+// swizzle for d = 64: piece ^ (row / 2 & 3)), so that the lanes of a load fall on
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  if constexpr (D == 128) return row * 128 + ((piece ^ (row & 7)) << 4);
+  if constexpr (D == 64) return row * 64 + ((piece ^ (row >> 1 & 3)) << 4);
+  return row * 16;
+}
+
+// First element of lane-quad t's key word w.  Dot products do not depend on
+// the order of d; this one reads whole pieces, and with the swizzle above the
+// two rows and four pieces of 8 lanes fall on all 32 banks.
+template <int D>
+__device__ __forceinline__ int key_elem(int t, int w) {
+  if constexpr (D == 16) return 4 * t;
+  if constexpr (D == 64) return 16 * t + 4 * w;
+  return (2 * t + w / 4) * 16 + (w % 4) * 4;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+
+template <int D>
+__device__ __forceinline__ void load_key8(uint32_t (&w)[Q8Frag<D>::kKWords], uint32_t tile, int row, int t) {
+  if constexpr (D == 16) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(tile + row * 16 + 4 * t));
+  } else {
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      const uint4 x = lds128(tile + piece_at<D>(row, (D / 64) * t + j));
+      w[4 * j] = x.x;
+      w[4 * j + 1] = x.y;
+      w[4 * j + 2] = x.z;
+      w[4 * j + 3] = x.w;
+    }
+  }
+}
+
+// Lane-group g's values: elements [g D / 8, (g + 1) D / 8) of a row.
+template <int D>
+__device__ __forceinline__ void load_val8(uint32_t (&w)[Q8Frag<D>::kVWords], uint32_t tile, int row, int g) {
+  if constexpr (D == 16) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(tile + row * 16 + 2 * g));
+    w[0] = x;
+  } else if constexpr (D == 64) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(w[0]), "=r"(w[1])
+                 : "r"(tile + piece_at<D>(row, g >> 1) + (g & 1) * 8));
+  } else {
+    const uint4 x = lds128(tile + piece_at<D>(row, g));
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  }
+}
+
+// D += A * B for one 16x8x16 f16 tile, fp32 accumulators (warp-wide).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two fp32 -> packed f16x2, round to nearest even; `lo` goes to bits 0..15.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// A bf16 pair times a power of two, as an f16 pair.
+__device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w, float s) {
+  return pack_f16x2(q8::bf16_lo(w) * s, q8::bf16_hi(w) * s);
+}
+__device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+// Exponent that brings a largest magnitude (bf16 bits) to [2^14, 2^15): x 2^-e.
+__device__ __forceinline__ int f16_exp(uint32_t amax) {
+  if (amax == 0) return 0;
+  const int e = (int)(amax >> 7) - 127 - 14;
+  return e < -126 ? -126 : (e > 113 ? 113 : e);
+}
+
+// Shared memory of the merge: m, l and O of each warp (in the rings, once every warp is
+// done with its own), and what the CTAs of a cluster send to one another.
+template <int D, int NT, int NW>
+constexpr int q8_merge_bytes() {
+  return (int)sizeof(float) * NW * 8 * NT * (2 + D);
+}
+template <int D, int NT>
+constexpr int q8_peer_floats() { return kMaxCluster * 8 * NT * 2 + 8 * NT * D + 4 * kMaxCluster; }
+template <int D, int NT, int NW, int R>
+constexpr int q8_ring_bytes() {
+  constexpr int ring = NW * R * kTileRows * D, merge = q8_merge_bytes<D, NT, NW>();
+  return ((ring > merge ? ring : merge) + 15) / 16 * 16;
+}
+// All of it: rings, 2 words, barriers, with clusters the peers' part, and what it takes to start on
+// a 1024-byte boundary (the swizzle goes by the address).
+template <int D, int NT, int NW, int R>
+constexpr int q8_smem_bytes(bool clusters) {
+  return 1024 + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8 + (clusters ? 4 * q8_peer_floats<D, NT>() : 0);
+}
+
+// A CTA's shared memory may be written by its peers once it has begun: no memory is ordered by this.
+__device__ __forceinline__ void cluster_begun_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
+__device__ __forceinline__ void cluster_begun_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// Four elements of an output: sums against a maximum m.
+struct Four {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ Four() : m(-INFINITY), l(0.f), o(make_float4(0.f, 0.f, 0.f, 0.f)) {}
+  __device__ __forceinline__ void add(float s, float l2, const float4& o2) {
+    l += s * l2;
+    o.x += s * o2.x;
+    o.y += s * o2.y;
+    o.z += s * o2.z;
+    o.w += s * o2.w;
+  }
+  // the i-th four of the output; weights are in units of kWeightUnit, their sum is not
+  __device__ __forceinline__ void store(void* out, size_t i, int f32) const {
+    const float x = o.x * kWeightUnit / l, y = o.y * kWeightUnit / l;
+    const float z = o.z * kWeightUnit / l, w = o.w * kWeightUnit / l;
+    if (f32) reinterpret_cast<float4*>(out)[i] = make_float4(x, y, z, w);
+    else reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
+  }
+};
+
+// Running softmax state of one n-tile (8 heads) of a warp: lane (g, t) holds
+// heads 2t and 2t + 1; O rows (mt, g) and (mt, g + 8) are elements
+// g D / 8 + 2 mt and the next one.
+template <int D>
+struct State {
+  float m[2], l[2];
+  float o[Q8Frag<D>::kMTiles][4];
+};
+
+// Factor of the scores from those of the head and of the keys, both > 0.  Kept
+// where a masked -inf stays -inf and a dot product of 0 stays 0.
+__device__ __forceinline__ float score_factor(float q, float k) { return fminf(fmaxf(q * k, 1e-37f), 1e37f); }
+
+// Dot products `x` (-inf where masked) of SUB blocks of 16 slots, to be multiplied
+// by f0, f1 (> 0, finite; heads 2t, 2t + 1) for scores in log2 units, with the value
+// scale 2^v -> weights as B fragments; updates m, l and rescales O.
+// GUARD: a column may have no unmasked row (else every one has).
+template <int D, int SUB, bool GUARD>
+__device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB][4], float f0, float f1, int v,
+                                             uint32_t (&pb)[SUB][2]) {
+  float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+  for (int u = 0; u < SUB; ++u) {
+    mx0 = fmaxf(mx0, fmaxf(x[u][0], x[u][2]));
+    mx1 = fmaxf(mx1, fmaxf(x[u][1], x[u][3]));
+  }
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+  }
+  const float fv = (float)v, inv = q8::exp2_int(-v);
+  const float n0 = fmaxf(st.m[0], fmaf(mx0, f0, fv)), n1 = fmaxf(st.m[1], fmaf(mx1, f1, fv));
+  // where nothing has been seen yet, exponents are taken against 0: all of them are of -inf
+  const float b0 = GUARD && n0 == -CUDART_INF_F ? 0.f : n0, b1 = GUARD && n1 == -CUDART_INF_F ? 0.f : n1;
+  const float a0 = fast_exp2(st.m[0] - b0), a1 = fast_exp2(st.m[1] - b1);
+  st.m[0] = n0;
+  st.m[1] = n1;
+  const float c0 = fv + kWeightExp - b0, c1 = fv + kWeightExp - b1;
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int u = 0; u < SUB; ++u) {
+    const float p0 = fast_exp2(fmaf(x[u][0], f0, c0)), p1 = fast_exp2(fmaf(x[u][1], f1, c1));
+    const float p2 = fast_exp2(fmaf(x[u][2], f0, c0)), p3 = fast_exp2(fmaf(x[u][3], f1, c1));
+    s0 += p0 + p2;
+    s1 += p1 + p3;
+    pb[u][0] = movmatrix_trans(pack_f16x2(p0, p1));
+    pb[u][1] = movmatrix_trans(pack_f16x2(p2, p3));
+  }
+  st.l[0] = st.l[0] * a0 + s0 * kWeightUnit * inv;
+  st.l[1] = st.l[1] * a1 + s1 * kWeightUnit * inv;
+  if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {   // a maximum moved
+#pragma unroll
+    for (int mt = 0; mt < Q8Frag<D>::kMTiles; ++mt) {
+      st.o[mt][0] *= a0;
+      st.o[mt][1] *= a1;
+      st.o[mt][2] *= a0;
+      st.o[mt][3] *= a1;
+    }
+  }
+}
+
+}  // namespace
+
+// NT = number of 8-column n-tiles; NW = warps; R = tiles (32 rows of keys or of
+// values) in a warp's ring; PER = CTAs an SM.
+//
+// CHUNK: attention of the first rows of a chunk instead of one token that is taken in.  The
+// columns of the products are then (row of the chunk, query head) pairs, up to 8 NT of them to
+// a CTA; a row at position start + t does not see the ring's slots that it has outlived (those
+// 1 .. t places after slot start mod W), and besides the tail's rows it sees the chunk's own up
+// to itself.  The cache stays as it is.
+template <int D, int NT, int NW, int R, int PER, int FMT, bool CHUNK>
+__global__ void __launch_bounds__(NW * 32, PER)
+swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
+  using F = Q8Frag<D>;
+  constexpr int kTile = kTileRows * D;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem_al = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024;
+  float* smem = reinterpret_cast<float*>(smem_al);
+
+  const int split = blockIdx.x, b = blockIdx.z;
+  const int kvh = CHUNK ? (int)blockIdx.y / p.groups : (int)blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int G = p.n_q_heads / p.n_kv_heads;
+  const int W = p.window;
+
+  // each warp streams its own blocks, K0 K1 V0 V1 of one after those of the other, through a
+  // ring of R tiles, one barrier a place, filled by TMA and freed by the warp itself
+  const uint32_t ring = tc::smem_u32(smem_al) + warp * R * kTile;
+  const uint32_t bars = tc::smem_u32(smem_al) + q8_ring_bytes<D, NT, NW, R>() + 16 + warp * R * 8;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) tc::mbar_init(bars + 8 * i, 1);
+    tc::mbar_fence_init();
+    tc::prefetch_map(&k_map);
+    tc::prefetch_map(&v_map);
+  }
+  __syncwarp();
+
+  wait_prior_grid();
+  allow_next_grid();
+  const size_t unit = (size_t)b * p.n_kv_heads + kvh;
+  // the CTA's columns: c0 .. c0 + cols - 1 of the pair's, and where column c's q and output rows are
+  const int c0 = CHUNK ? (int)(blockIdx.y % p.groups) * 8 * NT : 0;
+  const int cols = CHUNK ? min(8 * NT, p.max_tokens * G - c0) : G;
+  auto row_of = [&](int c) -> size_t {
+    if constexpr (!CHUNK) return unit * G + c;
+    const int tok = (c0 + c) / G;
+    return ((size_t)b * p.max_tokens + tok) * p.n_q_heads + (size_t)kvh * G + (c0 + c - tok * G);
+  };
+  // Q is asked for before the ring's tiles, which would keep it waiting for as long as it takes to
+  // fill every ring (about 4 us).  Lane (g, t) holds column 8 nt + g.
+  uint32_t qf[NT][2 * F::kKWords];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int c = nt * 8 + g;
+    const __nv_bfloat16* qrow = p.q + row_of(c < cols ? c : 0) * D;
+#pragma unroll
+    for (int w = 0; w < F::kKWords; ++w) {
+      const uint2 x = c < cols ? ldg_stream8(qrow + key_elem<D>(t, w)) : make_uint2(0, 0);
+      qf[nt][2 * w] = x.x;
+      qf[nt][2 * w + 1] = x.y;
+    }
+  }
+  uint4 fresh = make_uint4(0, 0, 0, 0);              // the new row, for the tail
+  if (!CHUNK && warp == NW - 1 && lane < 2 * (D / 8))
+    fresh = ldg_stream(reinterpret_cast<const uint4*>((lane < D / 8 ? p.k_new : p.v_new) + unit * D) + lane % (D / 8));
+  const long long pos = p.pos[b];
+  const int n_rows = CHUNK ? p.n_tokens[b] : 1;
+  if (pos < 0 || n_rows < 0 || (CHUNK && n_rows > p.max_tokens)) {
+    // every CTA of the sequence leaves here, whole clusters at a time
+    if (threadIdx.x == 0) raise_status(p.status, SWA_ERR_DEVICE_ARG);
+    return;
+  }
+  if (CHUNK && n_rows * G <= c0) return;             // no column of this CTA has a row
+  cluster_begun_arrive();                            // waited for before the first store to a peer
+  const int n_valid = (int)(pos + 1 < (long long)W ? pos + 1 : (long long)W);
+  const int s_new = (int)(pos % W);
+  const int blk0 = s_new / kQ8Block * kQ8Block;      // first slot of the block being filled
+  const int row_new = s_new - blk0;
+  const int r_begin = split * p.slots_per_split;     // a multiple of 64
+  const int r_stop = r_begin + p.slots_per_split;
+  const int r_end = r_stop < n_valid ? r_stop : n_valid;
+  const bool owner = s_new >= r_begin && s_new < r_stop;
+
+  const int n_blocks = (W + kQ8Block - 1) / kQ8Block;
+  const float* ksc = p.ring.k_scale + unit * n_blocks;
+  const float* vsc = p.ring.v_scale + unit * n_blocks;
+  __nv_bfloat16* kt = p.ring.k_tail + unit * kQ8Block * D;
+  __nv_bfloat16* vt = p.ring.v_tail + unit * kQ8Block * D;
+  // the new row, or the chunk's rows, new_stride elements apart
+  const __nv_bfloat16* kn = p.k_new + (CHUNK ? ((size_t)b * p.max_tokens * p.n_kv_heads + kvh) : unit) * D;
+  const __nv_bfloat16* vn = p.v_new + (CHUNK ? ((size_t)b * p.max_tokens * p.n_kv_heads + kvh) : unit) * D;
+  const size_t new_stride = (size_t)p.n_kv_heads * D;
+
+  // The new row goes in: into the tail now (no one reads that row there), or, if it fills its block up,
+  // with the tail into the ring when this CTA, the only one to read the tail, is done.
+  const bool fills = !CHUNK && owner && s_new + 1 == min(blk0 + kQ8Block, W);
+  if (!CHUNK && owner && !fills && warp == NW - 1 && lane < 2 * (D / 8)) {
+    const int i = lane % (D / 8);
+    reinterpret_cast<uint4*>((lane < D / 8 ? kt : vt) + (size_t)row_new * D)[i] = fresh;
+  }
+
+  // The warp's blocks: those of its split in turn.  Rows [first_row(x), r_end) of the block at
+  // slot x are held in 8 bits and in the window; the block being filled may have none.
+  auto first_row = [&](int x) { return x == blk0 ? s_new + 1 : x; };
+  const int skip = s_new + 1 >= min(blk0 + kQ8Block, n_valid) ? blk0 : -1;
+  auto next_block = [&](int x) {
+    x += NW * kQ8Block;
+    return x == skip ? x + NW * kQ8Block : x;
+  };
+  // Rows in bf16, 16 at a time to the warps of one CTA of the pair: those of the block being filled
+  // (the tail's and, if one token is taken in, the new row), then those of the chunk.  Their keys and
+  // values are the ring's first tiles (16 rows of bf16 are as large as 32 rows of bytes).
+  const int old_rows = CHUNK ? row_new : row_new + 1;
+  const int old_subs = (old_rows + kSub - 1) / kSub;
+  const int subs = owner ? old_subs + (CHUNK ? (n_rows + kSub - 1) / kSub : 0) : 0;
+  static_assert(!CHUNK || 2 * ((kQ8Block / kSub + (kChunkRows + kSub - 1) / kSub + NW - 1) / NW) <= R,
+                "a warp's rows in bf16 fit its ring");
+  // the tile after the last one issued: its block, which of the block's, its place in the ring
+  int is_x = next_block(r_begin + (warp - NW) * kQ8Block), is_i = 0, is_at = 0;
+  auto issue = [&]() {
+    if (is_x >= r_end) return;
+    if (lane == 0) {
+      tc::mbar_arrive_expect_tx(bars + 8 * is_at, kTile);
+      tc::tma_load_3d(ring + is_at * kTile, is_i < kTiles ? &k_map : &v_map, 0,
+                      is_x + (is_i % kTiles) * kTileRows, (int)unit, bars + 8 * is_at);
+    }
+    is_at = is_at + 1 == R ? 0 : is_at + 1;
+    if (++is_i == 2 * kTiles) {
+      is_i = 0;
+      is_x = next_block(is_x);
+    }
+  };
+  int x0 = is_x;
+  for (int e = warp; e < subs; e += NW) {
+    const bool old = !CHUNK || e < old_subs;
+    const int first = (old ? e : e - old_subs) * kSub;               // row of the tail or of the chunk
+    const int rows = min(kSub, (old ? old_rows : n_rows) - first);
+    const uint32_t row_bytes = 2 * D;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t dst = ring + is_at * kTile, bar = bars + 8 * is_at;
+      if (lane == 0) tc::mbar_arrive_expect_tx(bar, rows * row_bytes);
+      __syncwarp();
+      if (old) {
+        const int held = CHUNK ? rows : min(rows, row_new - first);  // of them in the tail
+        if (lane == 0 && held > 0)
+          tc::bulk_load(dst, (i == 0 ? kt : vt) + (size_t)first * D, held * row_bytes, bar);
+        if (lane == 0 && held < rows) tc::bulk_load(dst + held * row_bytes, i == 0 ? kn : vn, row_bytes, bar);
+      } else if (lane < rows) {
+        tc::bulk_load(dst + lane * row_bytes, (i == 0 ? kn : vn) + (first + lane) * new_stride, row_bytes, bar);
+      }
+      ++is_at;                                                       // at most R such tiles: is_at <= R
+    }
+  }
+  {
+    const int used = is_at;
+    if (is_at == R) is_at = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i >= used) issue();
+  }
+  float ks = 0.f, vs = 1.f;
+  if (x0 < r_end) {
+    ks = ksc[x0 / kQ8Block];
+    vs = vsc[x0 / kQ8Block];
+  }
+
+  // Q as the B operand of S^T = K Q^T, f16
+  float qs[NT][2];                                   // factor of the scores of columns 2t, 2t + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < 2 * F::kKWords; ++w) m = amax_word(m, qf[nt][w]);
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int e = f16_exp(m);
+    const float s = q8::exp2_int(-e);
+#pragma unroll
+    for (int w = 0; w < 2 * F::kKWords; ++w) qf[nt][w] = bf16_to_f16(qf[nt][w], s);
+    const float back = q8::exp2_int(e) * p.scale_log2;
+    qs[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+    qs[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+  }
+
+  int tok[NT][2];                                    // rows of the chunk that columns 2t, 2t + 1 belong to
+  if constexpr (CHUNK) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      tok[nt][0] = (c0 + nt * 8 + 2 * t) / G;
+      tok[nt][1] = (c0 + nt * 8 + 2 * t + 1) / G;
+    }
+  }
+
+  State<D> st[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    st[nt].m[0] = st[nt].m[1] = -CUDART_INF_F;
+    st[nt].l[0] = st[nt].l[1] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < F::kMTiles; ++mt) st[nt].o[mt][0] = st[nt].o[mt][1] = st[nt].o[mt][2] = st[nt].o[mt][3] = 0.f;
+  }
+
+  bool ok = true;
+  int at = 0, phase = 0;                       // place and phase of the next tile to read
+  // waits for the next tile (its address); once a wait has run out there is nothing more to wait for
+  auto take = [&]() -> uint32_t {
+    if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(bars + 8 * at, phase, p.status));
+    return ring + at * kTile;
+  };
+  // every lane has read the tile: the next one goes into its place
+  auto done = [&]() {
+    __syncwarp();
+    if (ok) issue();
+    if (++at == R) at = 0, phase ^= 1;
+  };
+  for (int e = warp; e < subs && ok; e += NW) {
+    const bool old = !CHUNK || e < old_subs;
+    const int first = (old ? e : e - old_subs) * kSub;
+    const int rows = min(kSub, (old ? old_rows : n_rows) - first);
+    uint32_t tile = take();
+    uint32_t tk[2][2 * F::kKWords], tv[4][F::kMTiles];
+    uint32_t km = 0, vm = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 8 + g;
+#pragma unroll
+      for (int w = 0; w < F::kKWords; ++w) {
+        uint2 x = lds64(tile + r * (2 * D) + 2 * key_elem<D>(t, w));
+        if (r >= rows) x = make_uint2(0, 0);
+        tk[i][2 * w] = x.x;
+        tk[i][2 * w + 1] = x.y;
+        km = amax_word(amax_word(km, x.x), x.y);
+      }
+    }
+    done();
+    tile = take();
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * t + (i & 1) + (i >> 1) * 8;
+#pragma unroll
+        for (int mt = 0; mt < F::kMTiles; ++mt) {
+          const uint32_t x = lds32(tile + r * (2 * D) + 2 * (g * (D / 8) + 2 * mt));
+          tv[i][mt] = r >= rows ? 0u : x;
+          vm = amax_word(vm, tv[i][mt]);
+        }
+      }
+      done();
+      const int ke = f16_exp(__reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16)));
+      const int ve = f16_exp(__reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16)));
+      const float kf = q8::exp2_int(-ke), vf = q8::exp2_int(-ve), ks16 = q8::exp2_int(ke);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int w = 0; w < 2 * F::kKWords; ++w) tk[i][w] = bf16_to_f16(tk[i][w], kf);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int mt = 0; mt < F::kMTiles; ++mt) tv[i][mt] = bf16_to_f16(tv[i][mt], vf);
+      const bool ok0 = g < rows, ok1 = 8 + g < rows;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int w = 0; w < F::kKWords; ++w)
+          mma_f16(x[0], tk[0][2 * w], tk[1][2 * w], tk[0][2 * w + 1], tk[1][2 * w + 1], qf[nt][2 * w],
+                  qf[nt][2 * w + 1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          bool see0 = ok0, see1 = ok1;
+          if constexpr (CHUNK) {
+            // a row of the tail, row_new - r places before the chunk, until W tokens have come after it;
+            // a row of the chunk from itself on
+            const int tc_ = tok[nt][c], r0 = first + g, r1 = r0 + 8;
+            see0 = see0 && (old ? tc_ < W - (row_new - r0) : tc_ >= r0);
+            see1 = see1 && (old ? tc_ < W - (row_new - r1) : tc_ >= r1);
+          }
+          if (!see0) x[0][c] = -CUDART_INF_F;
+          if (!see1) x[0][2 + c] = -CUDART_INF_F;
+        }
+        uint32_t pb[1][2];
+        softmax_step<D, 1, CHUNK>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), ve, pb);
+#pragma unroll
+        for (int mt = 0; mt < F::kMTiles; ++mt)
+          mma_f16(st[nt].o[mt], prmt(tv[0][mt], tv[1][mt], 0x5410), prmt(tv[0][mt], tv[1][mt], 0x7632),
+                  prmt(tv[2][mt], tv[3][mt], 0x5410), prmt(tv[2][mt], tv[3][mt], 0x7632), pb[0][0], pb[0][1]);
+      }
+    }
+  }
+
+  while (ok && x0 < r_end) {
+    const int lo = first_row(x0), hi = x0 + kQ8Block < r_end ? x0 + kQ8Block : r_end;
+    const bool partial = lo > x0 || hi < x0 + kQ8Block;
+    const int x1 = next_block(x0);
+    float ks1 = 0.f, vs1 = 1.f;                // the next block's scales, a block ahead
+    if (x1 < r_end) {
+      ks1 = ksc[x1 / kQ8Block];
+      vs1 = vsc[x1 / kQ8Block];
+    }
+
+    float x[NT][kSubs][4];
+#pragma unroll
+    for (int h = 0; h < kTiles; ++h) {
+      const uint32_t tile = take();
+      if (!ok) break;
+      // the tile goes to registers whole and its place is freed before the arithmetic: what a
+      // place holds while it waits to be read is not in flight
+      uint32_t kw[kTileSubs][2][F::kKWords];
+#pragma unroll
+      for (int s = 0; s < kTileSubs; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load_key8<D>(kw[s][i], tile, s * kSub + i * 8 + g, t);
+      done();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int s = 0; s < kTileSubs; ++s)
+          x[nt][h * kTileSubs + s][0] = x[nt][h * kTileSubs + s][1] = x[nt][h * kTileSubs + s][2] =
+              x[nt][h * kTileSubs + s][3] = 0.f;
+      // the sums of the tile's two mma blocks (and n-tiles) are independent chains
+#pragma unroll
+      for (int w = 0; w < F::kKWords; ++w) {
+#pragma unroll
+        for (int s = 0; s < kTileSubs; ++s) {
+          uint32_t a0, a1, a2, a3;
+          q8::unpack4<FMT>(kw[s][0][w], a0, a2);
+          q8::unpack4<FMT>(kw[s][1][w], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(x[nt][h * kTileSubs + s], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+        }
+      }
+    }
+    if (!ok) break;
+
+    uint32_t pb[NT][kSubs][2];
+    if constexpr (CHUNK) {
+      // the slot a places after s_new (round the ring) holds position start - W + a: seen by rows below a
+      const int a0 = x0 > s_new ? x0 - s_new : x0 - s_new + W;
+      if (partial || a0 < n_rows || (x0 <= s_new && s_new < x0 + kQ8Block)) {
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int slot = x0 + u * kSub + i * 8 + g, a = slot > s_new ? slot - s_new : slot - s_new + W;
+            const bool held = slot >= lo && slot < hi;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (!held || tok[nt][0] >= a) x[nt][u][2 * i] = -CUDART_INF_F;
+              if (!held || tok[nt][1] >= a) x[nt][u][2 * i + 1] = -CUDART_INF_F;
+            }
+          }
+        }
+      }
+    } else if (partial) {
+#pragma unroll
+      for (int u = 0; u < kSubs; ++u) {
+        const int r0 = x0 + u * kSub + g, r1 = r0 + 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (r0 < lo || r0 >= hi) x[nt][u][0] = x[nt][u][1] = -CUDART_INF_F;
+          if (r1 < lo || r1 >= hi) x[nt][u][2] = x[nt][u][3] = -CUDART_INF_F;
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      softmax_step<D, kSubs, CHUNK>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks), q8::exp_of(vs),
+                             pb[nt]);
+
+#pragma unroll
+    for (int h = 0; h < kTiles; ++h) {
+      const uint32_t tile = take();
+      if (!ok) break;
+      uint32_t vw[kTileSubs][4][F::kVWords];
+#pragma unroll
+      for (int s = 0; s < kTileSubs; ++s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_val8<D>(vw[s][i], tile, s * kSub + 2 * t + (i & 1) + (i >> 1) * 8, g);
+      }
+      done();
+      if (partial) {                           // 0 times what a masked row holds must be 0
+#pragma unroll
+        for (int s = 0; s < kTileSubs; ++s) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int slot = x0 + h * kTileRows + s * kSub + 2 * t + (i & 1) + (i >> 1) * 8;
+#pragma unroll
+            for (int w = 0; w < F::kVWords; ++w) vw[s][i][w] = slot < lo || slot >= hi ? 0u : vw[s][i][w];
+          }
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kTileSubs; ++s) {
+        const int u = h * kTileSubs + s;
+#pragma unroll
+        for (int mt = 0; mt < F::kMTiles; ++mt) {
+          // bytes 2 mt, 2 mt + 1 of rows (2t, 2t + 1) and (2t + 8, 2t + 9), paired by element
+          const uint32_t sel = (mt & 1) ? 0x7362 : 0x5140;
+          uint32_t a0, a1, a2, a3;
+          q8::unpack4<FMT>(prmt(vw[s][0][mt / 2], vw[s][1][mt / 2], sel), a0, a1);
+          q8::unpack4<FMT>(prmt(vw[s][2][mt / 2], vw[s][3][mt / 2], sel), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(st[nt].o[mt], a0, a1, a2, a3, pb[nt][u][0], pb[nt][u][1]);
+        }
+      }
+    }
+    if (!ok) break;
+    x0 = x1;
+    ks = ks1;
+    vs = vs1;
+  }
+  if (!ok) {
+    // a wait ran out (raised in the status word): give every copy still in flight its time to land
+    for (int i = 0; i < R; ++i) {
+      tc::mbar_wait(bars + 8 * at, phase, p.status);
+      if (++at == R) at = 0, phase ^= 1;
+    }
+  }
+
+  // ---- merge the NW warps of the CTA ----
+  // in the rings, once every warp is done with its own: (m, l)[NW][G8], then O[NW][G8][D] with the
+  // c-th four of a column h at c ^ (h / 2 & 3), so that the four columns of a store fall on different banks
+  __syncthreads();
+  constexpr int G8 = 8 * NT, D4 = D / 4;
+  float2* sm_ml = reinterpret_cast<float2*>(smem_al);
+  float4* sm_o = reinterpret_cast<float4*>(sm_ml + NW * G8);
+  uint32_t* red = reinterpret_cast<uint32_t*>(smem_al + q8_ring_bytes<D, NT, NW, R>());
+  // what the peers of a cluster send: O[rank][share], then (m, l)[rank][G8]
+  float4* peer_o = reinterpret_cast<float4*>(smem_al + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8);
+  float2* peer_ml = reinterpret_cast<float2*>(peer_o + G8 * D4 + kMaxCluster);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float l0 = st[nt].l[0], l1 = st[nt].l[1];
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int h = nt * 8 + 2 * t + e;
+      if (g == 0) sm_ml[warp * G8 + h] = make_float2(st[nt].m[e], e ? l1 : l0);
+      float4* o = sm_o + (warp * G8 + h) * D4;
+      if constexpr (D == 16) {                 // two elements a lane
+        reinterpret_cast<float2*>(o)[2 * ((g / 2) ^ t) + (g & 1)] = make_float2(st[nt].o[0][e], st[nt].o[0][2 + e]);
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < F::kMTiles; mt += 2)
+          o[(g * (D / 32) + mt / 2) ^ t] =
+              make_float4(st[nt].o[mt][e], st[nt].o[mt][2 + e], st[nt].o[mt + 1][e], st[nt].o[mt + 1][2 + e]);
+      }
+    }
+  }
+  __syncthreads();
+
+  cluster_begun_wait();
+  namespace cg = cooperative_groups;
+  cg::cluster_group cl = cg::this_cluster();
+  const int n_cl = p.cluster ? p.n_splits : 1, rank = p.cluster ? split : 0;
+  const int per = (cols * D4 + n_cl - 1) / n_cl;     // fours that a CTA of the cluster merges
+  const int live = CHUNK ? min(cols, n_rows * G - c0) : cols;   // columns with a row
+  for (int idx = threadIdx.x; idx < cols * D4; idx += NW * 32) {
+    const int h = idx / D4, c = idx % D4;
+    Four f;
+    float2 ml[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      ml[w] = sm_ml[w * G8 + h];
+      f.m = fmaxf(f.m, ml[w].x);
+    }
+    if (f.m != -CUDART_INF_F) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        f.add(fast_exp2(ml[w].x - f.m), ml[w].y, sm_o[(w * G8 + h) * D4 + (c ^ (h / 2 & 3))]);
+    }
+    if (p.n_splits == 1) {
+      if (h < live) f.store(p.out, row_of(h) * D4 + c, p.out_f32);
+    } else if (CHUNK || p.cluster) {
+      // each four to the CTA that merges it, m and l to all
+      cl.map_shared_rank(peer_o, idx / per)[rank * per + idx % per] = f.o;
+      for (int r = c; r < n_cl; r += D4) cl.map_shared_rank(peer_ml, r)[rank * G8 + h] = make_float2(f.m, f.l);
+    } else {
+      const size_t part = row_of(h) * p.n_splits + split;
+      reinterpret_cast<float4*>(p.ws_o)[part * D4 + c] = f.o;
+      if (c == 0) reinterpret_cast<float2*>(p.ws_ml)[part] = make_float2(f.m, f.l);
+    }
+  }
+
+  if (p.cluster) {
+    cl.sync();   // all has been sent; every CTA of the pair's cluster comes here
+    for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < live * D4; idx += NW * 32) {
+      const int h = idx / D4;
+      Four f;
+      for (int r = 0; r < n_cl; ++r) f.m = fmaxf(f.m, peer_ml[r * G8 + h].x);
+      for (int r = 0; r < n_cl; ++r) {
+        const float2 ml = peer_ml[r * G8 + h];
+        f.add(fast_exp2(ml.x - f.m), ml.y, peer_o[r * per + idx - rank * per]);
+      }
+      f.store(p.out, row_of(h) * D4 + idx % D4, p.out_f32);
+    }
+  }
+
+  if (fills) {
+    auto k_row = [&](int i) { return i == row_new ? kn : kt + (size_t)i * D; };
+    auto v_row = [&](int i) { return i == row_new ? vn : vt + (size_t)i * D; };
+    const size_t dst = (unit * W + blk0) * D;
+    q8::round_block<D, FMT, NW * 32>(k_row, v_row, row_new + 1, p.ring.k8 + dst, p.ring.v8 + dst,
+                                     p.ring.k_scale + unit * n_blocks + blk0 / kQ8Block,
+                                     p.ring.v_scale + unit * n_blocks + blk0 / kQ8Block, red);
+  }
+}
+
+// Merge of the per-split partials: grid B * Hq, a thread to four elements.
+template <int D>
+__global__ void __launch_bounds__(32) swa_q8_decode_combine_kernel(const Q8DecodeParams p) {
+  wait_prior_grid();
+  allow_next_grid();
+  const size_t bh = blockIdx.x;
+  const int c = threadIdx.x;
+  if (c >= D / 4 || p.pos[bh / p.n_q_heads] < 0) return;
+  const int S = p.n_splits;
+  const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + bh * S;
+  const float4* o = reinterpret_cast<const float4*>(p.ws_o) + bh * S * (D / 4) + c;
+  Four f;
+#pragma unroll 8
+  for (int s = 0; s < S; ++s) f.m = fmaxf(f.m, ml[s].x);
+#pragma unroll 8
+  for (int s = 0; s < S; ++s) f.add(fast_exp2(ml[s].x - f.m), ml[s].y, o[(size_t)s * (D / 4)]);
+  f.store(p.out, bh * (D / 4) + c, p.out_f32);
+}
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+template <int D, int NT, int V, int FMT, bool CHUNK>
+cudaError_t launch_t(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
+  constexpr int NW = kQ8Variants[V].warps, R = kQ8Variants[V].tiles;
+  constexpr int smem = q8_smem_bytes<D, NT, NW, R>(V == 0);   // only variant 0 comes in clusters
+  auto kern = swa_q8_decode_kernel<D, NT, NW, R, kQ8Variants[V].per_sm, FMT, CHUNK>;
+  if (smem > 48 * 1024) {
+    // raised once per device (the attribute persists for the process)
+    static bool set[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      set[dev] = true;
+    }
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.n_splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n_splits, p.n_kv_heads * p.groups, p.batch);
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, maps.k, maps.v);
+  if (e != cudaSuccess || p.n_splits == 1 || p.cluster) return e;
+  cudaLaunchConfig_t ccfg = {};
+  ccfg.gridDim = dim3((unsigned)((size_t)p.batch * p.n_q_heads));
+  ccfg.blockDim = dim3(32);
+  ccfg.stream = stream;
+  ccfg.attrs = attr;
+  ccfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&ccfg, swa_q8_decode_combine_kernel<D>, p);
+}
+
+// Variant 2 needs a kernel of at most 168 registers: not two n-tiles, nor the rows of a chunk.
+template <int D, int NT, int FMT, bool CHUNK>
+cudaError_t launch_v(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
+  if (p.variant == 0) return launch_t<D, NT, 0, FMT, CHUNK>(p, maps, stream);
+  if (p.variant == 1) return launch_t<D, NT, 1, FMT, CHUNK>(p, maps, stream);
+  if constexpr (NT == 1 && !CHUNK) {
+    if (p.variant == 2) return launch_t<D, NT, 2, FMT, CHUNK>(p, maps, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <int D, int FMT>
+cudaError_t launch_f(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
+  const int G = p.n_q_heads / p.n_kv_heads;
+  if (p.n_tokens != nullptr)
+    return p.max_tokens * G <= 8 ? launch_v<D, 1, FMT, true>(p, maps, stream) : launch_v<D, 2, FMT, true>(p, maps, stream);
+  return G <= 8 ? launch_v<D, 1, FMT, false>(p, maps, stream) : launch_v<D, 2, FMT, false>(p, maps, stream);
+}
+
+template <int D>
+cudaError_t launch_d(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
+  return p.ring.format == SWA_Q8_E4M3 ? launch_f<D, SWA_Q8_E4M3>(p, maps, stream)
+                                      : launch_f<D, SWA_Q8_INT8>(p, maps, stream);
+}
+
+}  // namespace
+}  // namespace swa

@@ -523,3 +523,32 @@ def test_bad_device_arguments_skip_the_sequence():
         swa.device_status()
     assert bool((o[0] == 9.0).all())
     torch.testing.assert_close(o[1], v[1, 0].float(), rtol=2.0 ** -10, atol=0)     # one key: the output is its value
+
+
+@pytest.mark.parametrize("B,H", [(19, 8), (37, 8), (41, 8), (70, 8), (5, 30)])
+def test_decode_in_every_variant_is_the_same_sequence_by_sequence(B, H):
+    """Batches that are spread over the SMs in different ways (one to three CTAs an SM, several waves, clusters): a
+    sequence's step does not depend on its neighbours beyond the order of fp32 sums."""
+    Hq, d, W = 2 * H, 64, 200
+    g = torch.Generator(device=DEV).manual_seed(B)
+    dims, one = (swa.Dims(n, Hq, H, d, W, 0.125, "f32") for n in (B, 1))
+    cache = swa.new_cache_q8(dims, "e4m3", DEV)
+    start = torch.randint(0, 500, (B,), generator=torch.Generator().manual_seed(B)).tolist()
+    for s in range(0, 500, W):
+        n = [max(0, min(W, x - s)) for x in start]
+        k, v = (torch.randn(B, W, H, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+        swa.cache_append_q8(dims, cache, k, v, i32([s] * B), i32(n))
+    q, k, v = (torch.randn(B, h, d, generator=g, device=DEV).to(torch.bfloat16) for h in (Hq, H, H))
+    parts = [cache.k, cache.v, cache.k_scale, cache.v_scale, cache.k_tail, cache.v_tail]
+    single = [swa.CacheQ8(*[(t.view(torch.int8) if t.dtype == torch.float8_e4m3fn else t)[b:b + 1].clone().view(t.dtype)
+                            for t in parts]) for b in range(B)]
+    out = torch.empty(B, Hq, d, device=DEV)
+    swa.decode_q8(dims, out, q, k, v, cache, i32(start), swa.decode_workspace_q8(dims, DEV))
+    for b in range(B):
+        o = torch.empty(1, Hq, d, device=DEV)
+        swa.decode_q8(one, o, q[b:b + 1], k[b:b + 1], v[b:b + 1], single[b], i32([start[b]]), swa.decode_workspace_q8(one, DEV))
+        # weights of f16, each within 2^-11, twice
+        assert float((o[0] - out[b]).abs().max()) <= 2.0 ** -10 * 5.0
+        assert torch.equal(single[b].k.view(torch.int8)[0], cache.k.view(torch.int8)[b])
+        assert torch.equal(single[b].k_tail[0], cache.k_tail[b]) and torch.equal(single[b].v_scale[0], cache.v_scale[b])
+    swa.device_status()
