@@ -178,8 +178,7 @@ struct Q8DecodeParams {
 struct Q8Variant {
   int warps, tiles, per_sm;
 };
-constexpr Q8Variant kQ8Variants[3] = {{8, 6, 1}, {4, 6, 2}, {4, 4, 3}};
-constexpr int kQ8TileRows = 32;        // rows of a tile
+constexpr Q8Variant kQ8Variants[3] = {{8, 3, 1}, {4, 3, 2}, {4, 2, 3}};
 constexpr int kQ8MaxCluster = 8;       // portable cluster size
 constexpr int kQ8FewColumns = 128;     // of a chunk that goes over the ring's bytes
 // Split of the W slots of one (sequence, kv head); a function of the shape.
@@ -192,7 +191,7 @@ Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int head_di
 int q8_few_columns();
 int q8_chunk_groups(int columns);
 // TMA descriptors of the ring's keys and values: [B * Hkv][W][d] bytes, boxes of
-// kQ8TileRows rows, swizzled by the row's size.
+// kQ8Block rows, swizzled by the row's size.
 struct Q8DecodeMaps {
   CUtensorMap k, v;
 };

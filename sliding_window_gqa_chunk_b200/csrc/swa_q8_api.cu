@@ -94,8 +94,8 @@ int launch_over_ring(swa::Q8DecodeParams& p, const swa_dims* dims, const swa_q8_
   if (rc) return rc;
   swa::Q8DecodeMaps maps;
   const long long pairs = (long long)dims->batch * dims->n_kv_heads;
-  if ((rc = swa::api_encode_bytes(&maps.k, cache->k, dims->head_dim, dims->window, pairs, swa::kQ8TileRows, "cache k"))) return rc;
-  if ((rc = swa::api_encode_bytes(&maps.v, cache->v, dims->head_dim, dims->window, pairs, swa::kQ8TileRows, "cache v"))) return rc;
+  if ((rc = swa::api_encode_bytes(&maps.k, cache->k, dims->head_dim, dims->window, pairs, swa::kQ8Block, "cache k"))) return rc;
+  if ((rc = swa::api_encode_bytes(&maps.v, cache->v, dims->head_dim, dims->window, pairs, swa::kQ8Block, "cache v"))) return rc;
   const cudaError_t e = swa::launch_q8_decode(p, maps, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, what);
   return swa::api_ok();

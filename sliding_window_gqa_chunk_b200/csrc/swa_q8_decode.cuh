@@ -27,7 +27,7 @@
 //
 // Bytes.  The bound is HBM: 538 MB for 64 sequences of W = 4096 with 8 kv heads of 128
 // take 88 us (6.1 TB/s of 6.56 measured for a copy).  Each warp streams its blocks through
-// a ring of its own in shared memory, 6 tiles of 32 rows, filled by TMA and freed by the
+// a ring of its own in shared memory, 3 tiles of 64 rows, filled by TMA and freed by the
 // warp when the tile is in registers; no warp waits for another before the merge.  8 warps
 // an SM keep 192 KB in flight.  Loads into registers with 12 warps an SM took 172 us; rings of
 // 12 KB for 16 warps 100 us (the arithmetic of a block is as long as a ring).
@@ -56,9 +56,6 @@ namespace {
 
 constexpr int kSub = 16;            // slots of one mma block
 constexpr int kSubs = kQ8Block / kSub;        // mma blocks of a scale block
-constexpr int kTileRows = kQ8TileRows;        // rows of a TMA tile
-constexpr int kTileSubs = kTileRows / kSub;
-constexpr int kTiles = kQ8Block / kTileRows;  // tiles of a block's keys (and of its values)
 constexpr int kMaxCluster = kQ8MaxCluster;
 constexpr float kWeightExp = 15.f;  // the largest weight is 2^15
 constexpr float kWeightUnit = 1.f / 32768.f;
@@ -185,7 +182,7 @@ template <int D, int NT>
 constexpr int q8_peer_floats() { return kMaxCluster * 8 * NT * 2 + 8 * NT * D + 4 * kMaxCluster; }
 template <int D, int NT, int NW, int R>
 constexpr int q8_ring_bytes() {
-  constexpr int ring = NW * R * kTileRows * D, merge = q8_merge_bytes<D, NT, NW>();
+  constexpr int ring = NW * R * kQ8Block * D, merge = q8_merge_bytes<D, NT, NW>();
   return ((ring > merge ? ring : merge) + 15) / 16 * 16;
 }
 // All of it: rings, 2 words, barriers, with clusters the peers' part, and what it takes to start on
@@ -284,7 +281,7 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
 
 }  // namespace
 
-// NT = number of 8-column n-tiles; NW = warps; R = tiles (32 rows of keys or of
+// NT = number of 8-column n-tiles; NW = warps; R = tiles (a block's keys or
 // values) in a warp's ring; PER = CTAs an SM.
 //
 // CHUNK: attention of the first rows of a chunk instead of one token that is taken in.  The
@@ -297,7 +294,7 @@ __global__ void __launch_bounds__(NW * 32, PER)
 swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
   using F = Q8Frag<D>;
-  constexpr int kTile = kTileRows * D;
+  constexpr int kTile = kQ8Block * D;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem_al = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024;
   float* smem = reinterpret_cast<float*>(smem_al);
@@ -309,7 +306,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   const int G = p.n_q_heads / p.n_kv_heads;
   const int W = p.window;
 
-  // each warp streams its own blocks, K0 K1 V0 V1 of one after those of the other, through a
+  // each warp streams its own blocks, keys and values of one after those of the other, through a
   // ring of R tiles, one barrier a place, filled by TMA and freed by the warp itself
   const uint32_t ring = tc::smem_u32(smem_al) + warp * R * kTile;
   const uint32_t bars = tc::smem_u32(smem_al) + q8_ring_bytes<D, NT, NW, R>() + 16 + warp * R * 8;
@@ -395,39 +392,37 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     return x == skip ? x + NW * kQ8Block : x;
   };
   // Rows in bf16, 16 at a time to the warps of one CTA of the pair: those of the block being filled
-  // (the tail's and, if one token is taken in, the new row), then those of the chunk.  Their keys and
-  // values are the ring's first tiles (16 rows of bf16 are as large as 32 rows of bytes).
+  // (the tail's and, if one token is taken in, the new row), then those of the chunk.  They come first in
+  // the ring, keys and values in one place (16 rows of bf16 are half as large as a block of bytes).
   const int old_rows = CHUNK ? row_new : row_new + 1;
   const int old_subs = (old_rows + kSub - 1) / kSub;
   const int subs = owner ? old_subs + (CHUNK ? (n_rows + kSub - 1) / kSub : 0) : 0;
-  static_assert(!CHUNK || 2 * ((kQ8Block / kSub + (kChunkRows + kSub - 1) / kSub + NW - 1) / NW) <= R,
+  static_assert((kQ8Block / kSub + (CHUNK ? (kChunkRows + kSub - 1) / kSub : 0) + NW - 1) / NW <= R,
                 "a warp's rows in bf16 fit its ring");
-  // the tile after the last one issued: its block, which of the block's, its place in the ring
-  int is_x = next_block(r_begin + (warp - NW) * kQ8Block), is_i = 0, is_at = 0;
+  // the tile after the last one issued: its block, keys or values, its place in the ring
+  int is_x = next_block(r_begin + (warp - NW) * kQ8Block), is_at = 0;
+  bool is_v = false;
   auto issue = [&]() {
     if (is_x >= r_end) return;
     if (lane == 0) {
       tc::mbar_arrive_expect_tx(bars + 8 * is_at, kTile);
-      tc::tma_load_3d(ring + is_at * kTile, is_i < kTiles ? &k_map : &v_map, 0,
-                      is_x + (is_i % kTiles) * kTileRows, (int)unit, bars + 8 * is_at);
+      tc::tma_load_3d(ring + is_at * kTile, is_v ? &v_map : &k_map, 0, is_x, (int)unit, bars + 8 * is_at);
     }
     is_at = is_at + 1 == R ? 0 : is_at + 1;
-    if (++is_i == 2 * kTiles) {
-      is_i = 0;
-      is_x = next_block(is_x);
-    }
+    if (is_v) is_x = next_block(is_x);
+    is_v = !is_v;
   };
   int x0 = is_x;
   for (int e = warp; e < subs; e += NW) {
     const bool old = !CHUNK || e < old_subs;
     const int first = (old ? e : e - old_subs) * kSub;               // row of the tail or of the chunk
     const int rows = min(kSub, (old ? old_rows : n_rows) - first);
-    const uint32_t row_bytes = 2 * D;
+    const uint32_t row_bytes = 2 * D, bar = bars + 8 * is_at;
+    if (lane == 0) tc::mbar_arrive_expect_tx(bar, 2 * rows * row_bytes);
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t dst = ring + is_at * kTile, bar = bars + 8 * is_at;
-      if (lane == 0) tc::mbar_arrive_expect_tx(bar, rows * row_bytes);
-      __syncwarp();
+      const uint32_t dst = ring + is_at * kTile + i * (kTile / 2);
       if (old) {
         const int held = CHUNK ? rows : min(rows, row_new - first);  // of them in the tail
         if (lane == 0 && held > 0)
@@ -436,8 +431,8 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       } else if (lane < rows) {
         tc::bulk_load(dst + lane * row_bytes, (i == 0 ? kn : vn) + (first + lane) * new_stride, row_bytes, bar);
       }
-      ++is_at;                                                       // at most R such tiles: is_at <= R
     }
+    ++is_at;                                                         // at most R of these: is_at <= R
   }
   {
     const int used = is_at;
@@ -506,7 +501,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     const bool old = !CHUNK || e < old_subs;
     const int first = (old ? e : e - old_subs) * kSub;
     const int rows = min(kSub, (old ? old_rows : n_rows) - first);
-    uint32_t tile = take();
+    const uint32_t tile = take();
     uint32_t tk[2][2 * F::kKWords], tv[4][F::kMTiles];
     uint32_t km = 0, vm = 0;
 #pragma unroll
@@ -521,15 +516,13 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         km = amax_word(amax_word(km, x.x), x.y);
       }
     }
-    done();
-    tile = take();
     if (ok) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 2 * t + (i & 1) + (i >> 1) * 8;
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt) {
-          const uint32_t x = lds32(tile + r * (2 * D) + 2 * (g * (D / 8) + 2 * mt));
+          const uint32_t x = lds32(tile + kTile / 2 + r * (2 * D) + 2 * (g * (D / 8) + 2 * mt));
           tv[i][mt] = r >= rows ? 0u : x;
           vm = amax_word(vm, tv[i][mt]);
         }
@@ -588,39 +581,33 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     }
 
     float x[NT][kSubs][4];
+    uint32_t tile = take();
+    if (!ok) break;
 #pragma unroll
-    for (int h = 0; h < kTiles; ++h) {
-      const uint32_t tile = take();
-      if (!ok) break;
-      // the tile goes to registers whole and its place is freed before the arithmetic: what a
-      // place holds while it waits to be read is not in flight
-      uint32_t kw[kTileSubs][2][F::kKWords];
+    for (int u = 0; u < kSubs; u += 2) {
+      // two mma blocks (and the n-tiles) at a time, whose sums are independent chains
+      uint32_t kw[2][2][F::kKWords];
 #pragma unroll
-      for (int s = 0; s < kTileSubs; ++s)
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) load_key8<D>(kw[s][i], tile, s * kSub + i * 8 + g, t);
-      done();
+        for (int i = 0; i < 2; ++i) load_key8<D>(kw[s][i], tile, (u + s) * kSub + i * 8 + g, t);
+      if (u + 2 == kSubs) done();              // the tile is in registers: its place is free before the arithmetic
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int s = 0; s < kTileSubs; ++s)
-          x[nt][h * kTileSubs + s][0] = x[nt][h * kTileSubs + s][1] = x[nt][h * kTileSubs + s][2] =
-              x[nt][h * kTileSubs + s][3] = 0.f;
-      // the sums of the tile's two mma blocks (and n-tiles) are independent chains
+        for (int s = 0; s < 2; ++s) x[nt][u + s][0] = x[nt][u + s][1] = x[nt][u + s][2] = x[nt][u + s][3] = 0.f;
 #pragma unroll
       for (int w = 0; w < F::kKWords; ++w) {
 #pragma unroll
-        for (int s = 0; s < kTileSubs; ++s) {
+        for (int s = 0; s < 2; ++s) {
           uint32_t a0, a1, a2, a3;
           q8::unpack4<FMT>(kw[s][0][w], a0, a2);
           q8::unpack4<FMT>(kw[s][1][w], a1, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(x[nt][h * kTileSubs + s], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+          for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt][u + s], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
         }
       }
     }
-    if (!ok) break;
 
     uint32_t pb[NT][kSubs][2];
     if constexpr (CHUNK) {
@@ -657,31 +644,30 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       softmax_step<D, kSubs, CHUNK>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks), q8::exp_of(vs),
                              pb[nt]);
 
+    tile = take();
+    if (!ok) break;
 #pragma unroll
-    for (int h = 0; h < kTiles; ++h) {
-      const uint32_t tile = take();
-      if (!ok) break;
-      uint32_t vw[kTileSubs][4][F::kVWords];
+    for (int u = 0; u < kSubs; u += 2) {
+      uint32_t vw[2][4][F::kVWords];
 #pragma unroll
-      for (int s = 0; s < kTileSubs; ++s) {
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_val8<D>(vw[s][i], tile, s * kSub + 2 * t + (i & 1) + (i >> 1) * 8, g);
-      }
-      done();
+        for (int i = 0; i < 4; ++i)
+          load_val8<D>(vw[s][i], tile, (u + s) * kSub + 2 * t + (i & 1) + (i >> 1) * 8, g);
+      if (u + 2 == kSubs) done();
       if (partial) {                           // 0 times what a masked row holds must be 0
 #pragma unroll
-        for (int s = 0; s < kTileSubs; ++s) {
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int slot = x0 + h * kTileRows + s * kSub + 2 * t + (i & 1) + (i >> 1) * 8;
+            const int slot = x0 + (u + s) * kSub + 2 * t + (i & 1) + (i >> 1) * 8;
 #pragma unroll
             for (int w = 0; w < F::kVWords; ++w) vw[s][i][w] = slot < lo || slot >= hi ? 0u : vw[s][i][w];
           }
         }
       }
 #pragma unroll
-      for (int s = 0; s < kTileSubs; ++s) {
-        const int u = h * kTileSubs + s;
+      for (int s = 0; s < 2; ++s) {
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt) {
           // bytes 2 mt, 2 mt + 1 of rows (2t, 2t + 1) and (2t + 8, 2t + 9), paired by element
@@ -690,11 +676,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
           q8::unpack4<FMT>(prmt(vw[s][0][mt / 2], vw[s][1][mt / 2], sel), a0, a1);
           q8::unpack4<FMT>(prmt(vw[s][2][mt / 2], vw[s][3][mt / 2], sel), a2, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(st[nt].o[mt], a0, a1, a2, a3, pb[nt][u][0], pb[nt][u][1]);
+          for (int nt = 0; nt < NT; ++nt) mma_f16(st[nt].o[mt], a0, a1, a2, a3, pb[nt][u + s][0], pb[nt][u + s][1]);
         }
       }
     }
-    if (!ok) break;
     x0 = x1;
     ks = ks1;
     vs = vs1;
