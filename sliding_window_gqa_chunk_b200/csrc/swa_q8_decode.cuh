@@ -147,11 +147,21 @@ __device__ __forceinline__ void load_val8(uint32_t (&w)[Q8Frag<D>::kVWords], uin
 // D += A * B for one 16x8x16 f16 tile, fp32 accumulators (warp-wide).
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = A * B: the first product of a sum.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Two fp32 -> packed f16x2, round to nearest even; `lo` goes to bits 0..15.
@@ -297,7 +307,6 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   constexpr int kTile = kQ8Block * D;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem_al = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023)) % 1024;
-  float* smem = reinterpret_cast<float*>(smem_al);
 
   const int split = blockIdx.x, b = blockIdx.z;
   const int kvh = CHUNK ? (int)blockIdx.y / p.groups : (int)blockIdx.y;
@@ -321,6 +330,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
 
   wait_prior_grid();
   allow_next_grid();
+  asm volatile("fence.proxy.async.global;" ::: "memory");   // earlier kernels' rows, for the copies below
   const size_t unit = (size_t)b * p.n_kv_heads + kvh;
   // the CTA's columns: c0 .. c0 + cols - 1 of the pair's, and where column c's q and output rows are
   const int c0 = CHUNK ? (int)(blockIdx.y % p.groups) * 8 * NT : 0;
@@ -593,10 +603,6 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         for (int i = 0; i < 2; ++i) load_key8<D>(kw[s][i], tile, (u + s) * kSub + i * 8 + g, t);
       if (u + 2 == kSubs) done();              // the tile is in registers: its place is free before the arithmetic
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) x[nt][u + s][0] = x[nt][u + s][1] = x[nt][u + s][2] = x[nt][u + s][3] = 0.f;
-#pragma unroll
       for (int w = 0; w < F::kKWords; ++w) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -604,7 +610,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
           q8::unpack4<FMT>(kw[s][0][w], a0, a2);
           q8::unpack4<FMT>(kw[s][1][w], a1, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt][u + s], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (w == 0) mma_f16_first(x[nt][u + s], a0, a1, a2, a3, qf[nt][0], qf[nt][1]);
+            else mma_f16(x[nt][u + s], a0, a1, a2, a3, qf[nt][2 * w], qf[nt][2 * w + 1]);
+          }
         }
       }
     }
