@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kAppendThreads) swa_q8_append_kernel(const Q8A
   allow_next_grid();
   const int kvh = blockIdx.y, b = blockIdx.z;
   const int W = p.window;
-  const long long s = p.start_pos[b];
+  const int s = p.start_pos[b];
   const int n = p.n_tokens[b];
   if (s < 0 || n < 0 || n > p.max_tokens) {
     if (threadIdx.x == 0) raise_status(p.status, SWA_ERR_DEVICE_ARG);
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kAppendThreads) swa_q8_append_kernel(const Q8A
   }
   if (n == 0) return;
   const int n_blocks = (W + kQ8Block - 1) / kQ8Block;
-  const int s_slot = (int)(s % W);
+  const int s_slot = (int)((uint32_t)s % (uint32_t)W);
   int j = s_slot / kQ8Block + (int)blockIdx.x;   // gridDim.x <= n_blocks
   if (j >= n_blocks) j -= n_blocks;
   const int first = j * kQ8Block;
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kAppendThreads) swa_q8_append_kernel(const Q8A
   if (blockIdx.x != 0) return;
 
   // the block that the last token leaves unfilled: its rows that the chunk brings
-  const int e_slot = (int)((s + n - 1) % W);
+  const int e_slot = (int)(((uint32_t)s + (uint32_t)(n - 1)) % (uint32_t)W);   // below 2^32: n <= W <= 2^30
   const int e_row = e_slot % kQ8Block;
   if (e_slot + 1 == W || e_row + 1 == kQ8Block) return;
   __syncthreads();                               // the tail's old rows have been read
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(kExpandThreads) swa_q8_expand_kernel(const Q8E
     }
   }
   const float ks = p.ring.k_scale[unit * n_blocks + j], vs = p.ring.v_scale[unit * n_blocks + j];
-  const long long s = p.start_pos[b];
+  const int s = p.start_pos[b];
   const int n = p.n_tokens[b];
   if (s <= 0 || n <= 0 || n > p.max_tokens) return;   // nothing is read from the ring
-  const int held = s < W ? (int)s : W;                // slots [0, held) hold a position
+  const int held = s < W ? s : W;                     // slots [0, held) hold a position
   if (first >= (held + kKeyTile - 1) / kKeyTile * kKeyTile) return;
-  const int s_slot = (int)(s % W);
+  const int s_slot = (int)((uint32_t)s % (uint32_t)W);
   const int open = s_slot / kQ8Block == j ? s_slot - first : 0;   // rows that are in the tail
 #pragma unroll
   for (int m = 0; m < kPer; ++m) {

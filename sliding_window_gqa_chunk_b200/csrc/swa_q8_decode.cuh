@@ -357,7 +357,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   uint4 fresh = make_uint4(0, 0, 0, 0);              // the new row, for the tail
   if (!CHUNK && warp == NW - 1 && lane < 2 * (D / 8))
     fresh = ldg_stream(reinterpret_cast<const uint4*>((lane < D / 8 ? p.k_new : p.v_new) + unit * D) + lane % (D / 8));
-  const long long pos = p.pos[b];
+  const int pos = p.pos[b];
   const int n_rows = CHUNK ? p.n_tokens[b] : 1;
   if (pos < 0 || n_rows < 0 || (CHUNK && n_rows > p.max_tokens)) {
     // every CTA of the sequence leaves here, whole clusters at a time
@@ -366,8 +366,8 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
   if (CHUNK && n_rows * G <= c0) return;             // no column of this CTA has a row
   cluster_begun_arrive();                            // waited for before the first store to a peer
-  const int n_valid = (int)(pos + 1 < (long long)W ? pos + 1 : (long long)W);
-  const int s_new = (int)(pos % W);
+  const int n_valid = pos < W ? pos + 1 : W;
+  const int s_new = (int)((uint32_t)pos % (uint32_t)W);   // in 32 bits: a 64-bit remainder is a long subroutine
   const int blk0 = s_new / kQ8Block * kQ8Block;      // first slot of the block being filled
   const int row_new = s_new - blk0;
   const int r_begin = split * p.slots_per_split;     // a multiple of 64
