@@ -594,6 +594,8 @@ int api_encode_bytes(CUtensorMap* map, const void* ptr, int row_bytes, int rows,
 
 int api_check_dims(const swa_dims* dims) { return check_dims(dims); }
 
+int* api_trace() { return g_trace; }
+
 int api_check_ptrs(const char* names, std::initializer_list<const void*> ptrs) { return check_ptrs(names, ptrs); }
 
 int api_check_ptrs4(const char* names, std::initializer_list<const void*> ptrs) {

@@ -169,6 +169,7 @@ struct Q8DecodeParams {
   int max_tokens, groups;       // rows of a chunk, CTAs that share its columns
   int batch, n_q_heads, n_kv_heads, head_dim, window;
   int n_splits, slots_per_split;
+  int* trace;                   // fault switch of checked builds, else NULL
   int variant;                  // of kQ8Variants
   int cluster;                  // 1: the splits of a pair merge in a thread-block cluster
   float scale_log2;             // scale * log2(e)
@@ -224,6 +225,7 @@ int api_status_word(int** out);
 int api_encode_bytes(CUtensorMap* map, const void* ptr, int row_bytes, int rows, long long n, int box_rows,
                      const char* what);
 int api_check_dims(const struct swa_dims* dims);
+int* api_trace();   // what swa_debug_set_trace of checked builds was given, else NULL
 int api_check_ptrs(const char* names, std::initializer_list<const void*> ptrs);      // 16-byte aligned
 int api_check_ptrs4(const char* names, std::initializer_list<const void*> ptrs);     // 4-byte aligned
 int api_check_decode(const struct swa_dims* dims, const void* out, const void* q, const void* k_new,

@@ -86,6 +86,7 @@ int launch_over_ring(swa::Q8DecodeParams& p, const swa_dims* dims, const swa_q8_
   p.window = dims->window;
   p.n_splits = sp.n_splits;
   p.slots_per_split = sp.slots_per_split;
+  p.trace = swa::api_trace();
   p.variant = sp.variant;
   p.cluster = sp.cluster;
   p.scale_log2 = dims->scale * 1.4426950408889634f;

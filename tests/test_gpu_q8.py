@@ -552,3 +552,51 @@ def test_decode_in_every_variant_is_the_same_sequence_by_sequence(B, H):
         assert torch.equal(single[b].k.view(torch.int8)[0], cache.k.view(torch.int8)[b])
         assert torch.equal(single[b].k_tail[0], cache.k_tail[b]) and torch.equal(single[b].v_scale[0], cache.v_scale[b])
     swa.device_status()
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_step_is_right():
+    """The checked build (waits of about a millisecond) never asks for one warp's first tile: the step reports a timeout,
+    every warp leaves through the merge, and with the switch off the same library gives the oracle's step."""
+    import ctypes
+    import os
+
+    from sliding_window_gqa_chunk_b200.csrc import build as swa_build
+
+    so = swa_build.build(force=True, defines=["SWA_TEST_FAULTS", "SWA_WAIT_LIMIT_CYCLES=2000000LL"],
+                         out=os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libswa_q8_faults.so"))
+    lib = ctypes.CDLL(so)
+    P, D, C = ctypes.c_void_p, ctypes.POINTER(swa._CDims), ctypes.POINTER(swa._CCacheQ8)
+    lib.swa_q8_decode.argtypes = [D, P, P, P, P, C, P, P, ctypes.c_size_t, P]
+    lib.swa_device_status.argtypes = [P]
+    lib.swa_debug_set_trace.argtypes = [P]
+    lib.swa_debug_set_trace.restype = None
+    B, Hq, H, d, W = 2, 4, 2, 64, 1200          # clusters of several CTAs
+    g = torch.Generator().manual_seed(9)
+    dims, cache, ref = make(B, Hq, H, d, W, "e4m3")
+    pos = fill(dims, cache, ref, [W + 30, 900], g, 400)
+    q, k, v = torch.randn(B, Hq, d, generator=g).to(torch.bfloat16), rows(g, B, H, d), rows(g, B, H, d)
+    qd, kd, vd, pd, ws = q.to(DEV), k.to(DEV), v.to(DEV), i32(pos), swa.decode_workspace_q8(dims, DEV)
+    o = torch.zeros((B, Hq, d), device=DEV)
+
+    def step():
+        return lib.swa_q8_decode(ctypes.byref(dims._record), o.data_ptr(), qd.data_ptr(), kd.data_ptr(), vd.data_ptr(),
+                                 ctypes.byref(cache._record.c), pd.data_ptr(), ws.data_ptr(), ws.numel(), None)
+
+    flag = torch.ones(1, dtype=torch.int32, device=DEV)
+    lib.swa_debug_set_trace(flag.data_ptr())
+    try:
+        torch.cuda.synchronize()
+        assert step() == swa.SWA_OK
+        torch.cuda.synchronize()
+        assert lib.swa_device_status(None) == swa.SWA_ERR_TIMEOUT
+        assert lib.swa_device_status(None) == swa.SWA_OK
+        flag.zero_()
+        torch.cuda.synchronize()
+        assert step() == swa.SWA_OK              # the row is taken in again, where it already is
+        torch.cuda.synchronize()
+        assert lib.swa_device_status(None) == swa.SWA_OK
+    finally:
+        lib.swa_debug_set_trace(None)
+    want, spread = q8.decode(ref, q, k, v, pos, dims.scale)
+    close(o, want, spread, DECODE_REL, W * 2.0 ** -23 * 200, "after the timeout")
+    same_cache(cache, ref, "after the timeout")
