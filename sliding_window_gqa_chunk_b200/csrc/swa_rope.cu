@@ -20,7 +20,9 @@ namespace swa {
 
 namespace {
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;          // tokens of a CTA in a chunk
+constexpr int kMaxTokens = 16;      // tokens of a CTA
+constexpr int kCtasPerSm = 5;       // at 48 registers a thread
+constexpr int kSms = 148;
 constexpr int kMaxPairs = 64;       // rotary_dim <= 128
 
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -52,17 +54,18 @@ __device__ __forceinline__ void turn(uint4& a, uint4& b, const float (&cs)[8], c
 }
 }  // namespace
 
-// TOK tokens (of all B * T, numbered through) per CTA.
-template <bool INTER, int TOK>
-__global__ void __launch_bounds__(kThreads, 5) swa_rope_kernel(const RopeParams p) {
-  __shared__ float2 ang[TOK][kMaxPairs];
-  __shared__ int live[TOK];
+// `tokens` tokens (of all B * T, numbered through) per CTA; units * tokens * lanes threads, and those
+// that make it whole warps.
+template <bool INTER>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) swa_rope_kernel(const RopeParams p, int tokens, int lanes) {
+  __shared__ float2 ang[kMaxTokens][kMaxPairs];
+  __shared__ int live[kMaxTokens];
   wait_prior_grid();
   allow_next_grid();
   const int T = p.max_tokens, r2 = p.rotary_dim / 2;
-  const int first = blockIdx.x * TOK;
+  const int first = blockIdx.x * tokens;
   const int n_rows = p.batch * T;                     // below 2^31
-  for (int i = threadIdx.x; i < TOK * r2; i += kThreads) {
+  for (int i = threadIdx.x; i < tokens * r2; i += blockDim.x) {
     const int tok = first + i / r2, pair = i % r2;
     bool ok = false;
     if (tok < n_rows) {
@@ -83,12 +86,11 @@ __global__ void __launch_bounds__(kThreads, 5) swa_rope_kernel(const RopeParams 
   __syncthreads();
 
   // thread -> (unit c of a row, token, first head); the heads go in steps
-  const int units = p.head_dim / 16;                  // 1, 4 or 8: divides the threads
+  const int units = p.head_dim / 16;                  // 1, 4 or 8
   const int c = threadIdx.x % units;
-  const int tk = threadIdx.x / units % TOK;
-  const int lane = threadIdx.x / (units * TOK);
-  const int lanes = kThreads / (units * TOK);
-  if (!live[tk]) return;
+  const int tk = threadIdx.x / units % tokens;
+  const int lane = threadIdx.x / (units * tokens);
+  if (lane >= lanes || !live[tk]) return;
   const int tok = first + tk;
   const int rot = p.rotary_dim / 16;                  // units that are turned
   const bool turned = c < rot;
@@ -122,28 +124,26 @@ __global__ void __launch_bounds__(kThreads, 5) swa_rope_kernel(const RopeParams 
   }
 }
 
-namespace {
-template <bool INTER, int TOK>
-cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t stream) {
-  const long long rows = (long long)p.batch * p.max_tokens;
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
+  // As many tokens to a CTA as leave the last wave of CTAs full, 16 at most: 4096 tokens take one wave of 683
+  // CTAs of 6, @@ us, and @@ in one and a half of 4 each.
+  const long long rows = (long long)p.batch * p.max_tokens, slots = (long long)kSms * kCtasPerSm;
+  const long long waves = (rows + slots * kMaxTokens - 1) / (slots * kMaxTokens);
+  const int tokens = (int)((rows + slots * waves - 1) / (slots * waves));
+  const int units = p.head_dim / 16, heads = p.n_q_heads + p.n_kv_heads;
+  int lanes = kThreads / (units * tokens);
+  if (lanes > heads) lanes = heads;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows + TOK - 1) / TOK));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)((rows + tokens - 1) / tokens));
+  cfg.blockDim = dim3((unsigned)((units * tokens * lanes + 31) / 32 * 32));
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, swa_rope_kernel<INTER, TOK>, p);
-}
-}  // namespace
-
-cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
-  // one token per CTA until that fills the SMs several times over
-  if ((long long)p.batch * p.max_tokens < 148 * 8)
-    return p.interleaved ? launch_rope_t<true, 1>(p, stream) : launch_rope_t<false, 1>(p, stream);
-  return p.interleaved ? launch_rope_t<true, kTokens>(p, stream) : launch_rope_t<false, kTokens>(p, stream);
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, swa_rope_kernel<true>, p, tokens, lanes)
+                       : cudaLaunchKernelEx(&cfg, swa_rope_kernel<false>, p, tokens, lanes);
 }
 
 }  // namespace swa
