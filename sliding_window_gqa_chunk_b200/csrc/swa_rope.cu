@@ -5,7 +5,9 @@
 // chunks and the launch for a decode step.  The angles of a token are the same
 // for all its heads: the CTA computes the cos and sin of its tokens once into
 // shared memory, and each thread keeps those of its 8 pairs in registers
-// while it goes through its share of the heads.  A thread's unit is 16
+// while it goes through its share of the heads, two at a time: 4096 tokens of
+// 40 heads of 128 take 17.3 us (4.8 TB/s; 16384 tokens 58.4, 5.7 TB/s), one
+// head at a time with 5 CTAs an SM 18.1, three with 3 CTAs 17.9.  A thread's unit is 16
 // elements of a head, two 16-byte pieces that hold whole pairs: [8c, 8c + 8)
 // and [r/2 + 8c, ...) with halves, [16c, 16c + 16) interleaved; pair 8c + i is
 // the i-th of unit c either way.
@@ -21,7 +23,8 @@ namespace swa {
 namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;      // tokens of a CTA
-constexpr int kCtasPerSm = 5;       // at 48 registers a thread
+constexpr int kHeads = 2;           // heads of a thread whose loads are in flight together
+constexpr int kCtasPerSm = 4;       // at 64 registers a thread
 constexpr int kSms = 148;
 constexpr int kMaxPairs = 64;       // rotary_dim <= 128
 
@@ -90,10 +93,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) swa_rope_kernel(const Ro
   const int c = threadIdx.x % units;
   const int tk = threadIdx.x / units % tokens;
   const int lane = threadIdx.x / (units * tokens);
-  if (lane >= lanes || !live[tk]) return;
+  const bool turned = c < p.rotary_dim / 16;
+  if (lane >= lanes || !live[tk] || (!turned && p.q_in_place && p.k_in_place)) return;
   const int tok = first + tk;
-  const int rot = p.rotary_dim / 16;                  // units that are turned
-  const bool turned = c < rot;
   float cs[8], sn[8];
   if (turned) {
 #pragma unroll
@@ -112,21 +114,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) swa_rope_kernel(const Ro
   const __nv_bfloat16* k = p.k + (tok * p.k_stride - Hq * D);
   __nv_bfloat16* q_out = p.q_out + (size_t)tok * Hq * D;
   __nv_bfloat16* k_out = p.k_out + ((int64_t)tok * p.n_kv_heads - Hq) * D;
-  for (int h = lane; h < heads; h += lanes) {
-    const bool is_q = h < Hq;
-    if (!turned && (is_q ? p.q_in_place : p.k_in_place)) continue;
-    const __nv_bfloat16* src = (is_q ? q : k) + h * D;
-    __nv_bfloat16* dst = (is_q ? q_out : k_out) + h * D;
-    uint4 a = *reinterpret_cast<const uint4*>(src + e0), b = *reinterpret_cast<const uint4*>(src + e1);
-    if (turned) turn<INTER>(a, b, cs, sn);
-    *reinterpret_cast<uint4*>(dst + e0) = a;
-    *reinterpret_cast<uint4*>(dst + e1) = b;
+  for (int h0 = lane; h0 < heads; h0 += kHeads * lanes) {
+    uint4 a[kHeads], b[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = h0 + i * lanes;
+      if (h >= heads) break;
+      const __nv_bfloat16* src = (h < Hq ? q : k) + h * D;
+      a[i] = *reinterpret_cast<const uint4*>(src + e0);
+      b[i] = *reinterpret_cast<const uint4*>(src + e1);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = h0 + i * lanes;
+      if (h >= heads) break;
+      const bool is_q = h < Hq;
+      if (!turned && (is_q ? p.q_in_place : p.k_in_place)) continue;
+      __nv_bfloat16* dst = (is_q ? q_out : k_out) + h * D;
+      if (turned) turn<INTER>(a[i], b[i], cs, sn);
+      *reinterpret_cast<uint4*>(dst + e0) = a[i];
+      *reinterpret_cast<uint4*>(dst + e1) = b[i];
+    }
   }
 }
 
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
-  // As many tokens to a CTA as leave the last wave of CTAs full, 16 at most: 4096 tokens take one wave of 683
-  // CTAs of 6, @@ us, and @@ in one and a half of 4 each.
+  // As many tokens to a CTA as leave the last wave of CTAs full, 16 at most (24 and 32: the same up
+  // to 10 % slower): 4096 tokens take one wave of 586 CTAs of 7.
   const long long rows = (long long)p.batch * p.max_tokens, slots = (long long)kSms * kCtasPerSm;
   const long long waves = (rows + slots * kMaxTokens - 1) / (slots * kMaxTokens);
   const int tokens = (int)((rows + slots * waves - 1) / (slots * waves));

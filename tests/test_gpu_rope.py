@@ -33,8 +33,8 @@ def check(got, x, positions, spec, transpose=False):
     (1, 1, 4, 2, 16, 16, [0], [1]),
     (1, 1, 32, 8, 128, 128, [2 ** 31 - 2], [1]),
     (3, 7, 6, 2, 64, 32, [0, 5, 100000], [7, 0, 3]),
-    (2, 900, 3, 1, 128, 96, [2 ** 24 + 1, 31], [900, 611]),      # 3 tokens a CTA, 4 heads
-    (3, 3201, 2, 1, 64, 32, [0, 2 ** 20, 77], [3201, 3200, 17]), # 13 tokens a CTA
+    (2, 900, 3, 1, 128, 96, [2 ** 24 + 1, 31], [900, 611]),      # 4 tokens a CTA, 4 heads
+    (3, 3201, 2, 1, 64, 32, [0, 2 ** 20, 77], [3201, 3200, 17]), # 9 tokens a CTA
     (2, 6300, 1, 1, 16, 16, [5, 10 ** 9], [6300, 6299]),         # two waves of 9
     (2, 601, 7, 7, 64, 64, [2 ** 31 - 700, 9], [601, 601]),
     (70, 1, 9, 3, 128, 48, list(range(0, 7000, 100)), [1] * 70),
