@@ -66,13 +66,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) swa_rope_kernel(const Ro
   wait_prior_grid();
   allow_next_grid();
   const int T = p.max_tokens, r2 = p.rotary_dim / 2;
-  const int first = blockIdx.x * tokens;
-  const int n_rows = p.batch * T;                     // below 2^31
+  const uint32_t first = blockIdx.x * tokens;
+  const uint32_t n_rows = p.batch * T;                // below 2^31; the last CTA's tokens may pass it
   for (int i = threadIdx.x; i < tokens * r2; i += blockDim.x) {
-    const int tok = first + i / r2, pair = i % r2;
+    const uint32_t tok = first + i / r2;
+    const int pair = i % r2;
     bool ok = false;
     if (tok < n_rows) {
-      const int b = tok / T, t = tok - b * T;
+      const int b = (int)tok / T, t = (int)tok - b * T;
       const int s = p.start_pos[b], n = p.n_tokens != nullptr ? p.n_tokens[b] : T;
       if (s < 0 || n < 0 || n > T) {
         if (t == 0 && pair == 0) raise_status(p.status, SWA_ERR_DEVICE_ARG);
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) swa_rope_kernel(const Ro
   const int lane = threadIdx.x / (units * tokens);
   const bool turned = c < p.rotary_dim / 16;
   if (lane >= lanes || !live[tk] || (!turned && p.q_in_place && p.k_in_place)) return;
-  const int tok = first + tk;
+  const int tok = (int)first + tk;                    // a live one: below n_rows
   float cs[8], sn[8];
   if (turned) {
 #pragma unroll
