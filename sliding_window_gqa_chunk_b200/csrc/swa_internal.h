@@ -181,16 +181,19 @@ struct Q8Variant {
 };
 constexpr Q8Variant kQ8Variants[3] = {{8, 3, 1}, {4, 3, 2}, {4, 2, 3}};
 constexpr int kQ8MaxCluster = 8;       // portable cluster size
-constexpr int kQ8FewColumns = 128;     // of a chunk that goes over the ring's bytes
 // Split of the W slots of one (sequence, kv head); a function of the shape.
 struct Q8DecodeSplit {
   int n_splits, slots_per_split, variant, cluster;
 };
 Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int head_dim, int groups, bool chunk, bool wide);
-// Chunks of at most this many columns (rows x query heads of a kv head) go through launch_q8_decode
-// too, with q, k, v and out as in the prefill and start positions as pos.
-int q8_few_columns();
-int q8_chunk_groups(int columns);
+// The same with clusters of a size of which the current device holds as many as there are pairs at once.
+Q8DecodeSplit q8_fit_clusters(Q8DecodeSplit s, long long units, int window);
+// Clusters of `size` CTAs, one an SM, that the current device holds at once (0 if it cannot be told).
+int q8_clusters_at_once(int size);
+// A chunk of few columns (rows x query heads of a kv head) goes through launch_q8_decode too, with q, k, v
+// and out as in the prefill and start positions as pos: the CTAs that share a pair's columns; 0 where the
+// ring is written out for the prefill kernel instead.
+int q8_chunk_groups(long long rows, int group, long long pairs, int window);
 // TMA descriptors of the ring's keys and values: [B * Hkv][W][d] bytes, boxes of
 // kQ8Block rows, swizzled by the row's size.
 struct Q8DecodeMaps {

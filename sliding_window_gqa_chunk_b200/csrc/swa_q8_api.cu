@@ -72,8 +72,10 @@ swa::Q8DecodeSplit split_of(const swa_dims* dims, int groups, bool chunk) {
 
 // Fills in what decode steps and short chunks share, and launches.
 int launch_over_ring(swa::Q8DecodeParams& p, const swa_dims* dims, const swa_q8_cache* cache, void* out, const void* q,
-                     const void* k, const void* v, const int32_t* pos, const swa::Q8DecodeSplit& sp, void* stream,
+                     const void* k, const void* v, const int32_t* pos, const swa::Q8DecodeSplit& shape_split, void* stream,
                      const char* what) {
+  const swa::Q8DecodeSplit sp =
+      swa::q8_fit_clusters(shape_split, (long long)dims->batch * dims->n_kv_heads * p.groups, dims->window);
   p.out = out;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_new = static_cast<const __nv_bfloat16*>(k);
@@ -151,10 +153,10 @@ int swa_q8_prefill_chunk(const swa_dims* dims, void* out, const void* q, const v
   if (workspace_bytes < need)
     return swa::api_fail(SWA_ERR_WORKSPACE_TOO_SMALL, "q8 prefill workspace of %zu bytes, %zu needed",
                          workspace_bytes, need);
-  const long long columns = (long long)max_tokens * (dims->n_q_heads / dims->n_kv_heads);
-  const int groups = columns <= swa::q8_few_columns() ? swa::q8_chunk_groups((int)columns) : 0;
+  const int groups = swa::q8_chunk_groups(max_tokens, dims->n_q_heads / dims->n_kv_heads,
+                                          (long long)dims->batch * dims->n_kv_heads, dims->window);
   if (groups > 0 && (long long)dims->n_kv_heads * groups <= 65535) {   // CTAs along the grid's second axis
-    // a few rows: straight over the ring's bytes
+    // few columns: straight over the ring's bytes
     swa::Q8DecodeParams d;
     d.ring = p.ring;
     d.ws_o = d.ws_ml = nullptr;

@@ -64,12 +64,37 @@ Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int head_di
   return s;
 }
 
-// Columns (rows of the chunk times query heads of a kv head) up to which a chunk goes straight over
-// the ring's bytes, which each 16 of them read again, and is not written out in bf16 and attended to in
-// tiles of 128 rows.  At W = 4096, 32 query heads over 8, d = 128: 16 columns 35 us and 205 for 16
-// sequences; 128 columns 217 and 209 for 16 sequences, 23 and 48 for one.
-int q8_few_columns() { return kQ8FewColumns; }
-int q8_chunk_groups(int columns) { return columns > 8 ? (columns + 15) / 16 : 1; }
+// Clusters do not cross the borders of the GPU's clusters of SMs, so of the larger sizes 148 SMs hold less than
+// 148 CTAs (105 in clusters of 7, 120 of 8): pairs that do not all fit at once would take twice as long.
+// 16 pairs of 64 blocks: 12.3 us in clusters of 8, 8.6 of 6; 48 pairs: 20.5 us of 3, 14.3 of 2.
+Q8DecodeSplit q8_fit_clusters(Q8DecodeSplit s, long long units, int window) {
+  const long long n_blocks = ((long long)window + kQ8Block - 1) / kQ8Block;
+  for (int size = s.n_splits - 1; s.cluster && size >= 1; --size) {
+    const int room = q8_clusters_at_once(s.n_splits);
+    if (room == 0 || units <= room) break;
+    const long long per = (n_blocks + size - 1) / size;
+    s.slots_per_split = (int)(per * kQ8Block);
+    s.n_splits = (int)((n_blocks + per - 1) / per);
+    if (s.n_splits == 1) s.cluster = 0;
+  }
+  return s;
+}
+
+// A chunk's columns go straight over the ring's bytes, which each 16 of them read again, or the ring is
+// written out in bf16 and attended to in tiles of 128 rows, which a CTA takes 35 us for in a window of 4096
+// however few of them there are.  Over the bytes go up to 128 columns; what the SMs hold at once (up to 512
+// rows, which one CTA of a pair reads alone); and up to 256 columns of up to 64 rows in two waves (of windows
+// of up to 8192: the written-out way has less to do before the first key and less for each).  Measured over the
+// bytes and written out (us, W = 4096, d = 128; 32 query heads over 8): 16 sequences x 4 rows 29, 205; 16 x 32
+// rows 217, 209; 1 x 64 rows 27, 49; 2 x 64 49, 55; 4 x 33 54, 73; 4 x 48 79, 74; 1 x 128 51, 50.  4 over 1:
+// 1 x 512 rows 37, 42; 1 x 1024 88, 43.  1 over 1: 1 x 512 24, 38; 1 x 1024 40, 38; 1 x 2048 70, 37.  In two
+// waves: 8 over 8, W = 7215, 3 x 164 rows 99, 83; 16 over 4, W = 16270, 3 x 53 184, 116.
+int q8_chunk_groups(long long rows, int group, long long pairs, int window) {
+  const long long columns = rows * group, groups = columns > 8 ? (columns + 15) / 16 : 1, units = pairs * groups;
+  const bool over_bytes = columns <= 128 || (units <= kSms && rows <= 512) ||
+                          (units <= 2 * kSms && columns <= 256 && rows <= 64 && window <= 8192);
+  return over_bytes ? (int)groups : 0;
+}
 
 cudaError_t launch_q8_decode(const Q8DecodeParams& p, const Q8DecodeMaps& maps, cudaStream_t stream) {
   switch (p.head_dim) {

@@ -59,7 +59,6 @@ constexpr int kSubs = kQ8Block / kSub;        // mma blocks of a scale block
 constexpr int kMaxCluster = kQ8MaxCluster;
 constexpr float kWeightExp = 15.f;  // the largest weight is 2^15
 constexpr float kWeightUnit = 1.f / 32768.f;
-constexpr int kChunkRows = kQ8FewColumns;     // a chunk of so many columns has at most as many rows
 
 // Row fragments of a lane: bytes of a key row (D / 4) and of a value row (D / 8).
 template <int D>
@@ -402,13 +401,13 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     return x == skip ? x + NW * kQ8Block : x;
   };
   // Rows in bf16, 16 at a time to the warps of one CTA of the pair: those of the block being filled
-  // (the tail's and, if one token is taken in, the new row), then those of the chunk.  They come first in
-  // the ring, keys and values in one place (16 rows of bf16 are half as large as a block of bytes).
+  // (the tail's and, if one token is taken in, the new row), then those of the chunk up to the last that
+  // the CTA's columns belong to.  They come first in the ring, keys and values in one place (16 rows of
+  // bf16 are half as large as a block of bytes).
   const int old_rows = CHUNK ? row_new : row_new + 1;
   const int old_subs = (old_rows + kSub - 1) / kSub;
-  const int subs = owner ? old_subs + (CHUNK ? (n_rows + kSub - 1) / kSub : 0) : 0;
-  static_assert((kQ8Block / kSub + (CHUNK ? (kChunkRows + kSub - 1) / kSub : 0) + NW - 1) / NW <= R,
-                "a warp's rows in bf16 fit its ring");
+  const int seen_rows = CHUNK ? min(n_rows, (c0 + cols - 1) / G + 1) : 0;
+  const int subs = owner ? old_subs + (seen_rows + kSub - 1) / kSub : 0;
   // the tile after the last one issued: its block, keys or values, its place in the ring
   int is_x = next_block(r_begin + (warp - NW) * kQ8Block), is_at = 0;
   bool is_v = false;
@@ -429,10 +428,11 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     if (is_v) is_x = next_block(is_x);
     is_v = !is_v;
   };
-  for (int e = warp; e < subs; e += NW) {
-    const bool old = !CHUNK || e < old_subs;
-    const int first = (old ? e : e - old_subs) * kSub;               // row of the tail or of the chunk
-    const int rows = min(kSub, (old ? old_rows : n_rows) - first);
+  int is_e = warp;                                                   // the next 16 rows to issue
+  auto issue_rows = [&]() {
+    const bool old = !CHUNK || is_e < old_subs;
+    const int first = (old ? is_e : is_e - old_subs) * kSub;         // row of the tail or of the chunk
+    const int rows = min(kSub, (old ? old_rows : seen_rows) - first);
     const uint32_t row_bytes = 2 * D, bar = bars + 8 * is_at;
     if (lane == 0) tc::mbar_arrive_expect_tx(bar, 2 * rows * row_bytes);
     __syncwarp();
@@ -448,11 +448,12 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
         tc::bulk_load(dst + lane * row_bytes, (i == 0 ? kn : vn) + (first + lane) * new_stride, row_bytes, bar);
       }
     }
-    ++is_at;                                                         // at most R of these: is_at <= R
-  }
+    is_at = is_at + 1 == R ? 0 : is_at + 1;
+    is_e += NW;
+  };
   {
-    const int used = is_at;
-    if (is_at == R) is_at = 0;
+    int used = 0;
+    for (; is_e < subs && used < R; ++used) issue_rows();
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (i >= used) issue();
@@ -513,10 +514,16 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     if (ok) issue();
     if (++at == R) at = 0, phase ^= 1;
   };
+  auto done_rows = [&]() {
+    __syncwarp();
+    if (CHUNK && is_e < subs) issue_rows();
+    else issue();
+    if (++at == R) at = 0, phase ^= 1;
+  };
   for (int e = warp; e < subs && ok; e += NW) {
     const bool old = !CHUNK || e < old_subs;
     const int first = (old ? e : e - old_subs) * kSub;
-    const int rows = min(kSub, (old ? old_rows : n_rows) - first);
+    const int rows = min(kSub, (old ? old_rows : seen_rows) - first);
     const uint32_t tile = take();
     uint32_t tk[2][2 * F::kKWords], tv[4][F::kMTiles];
     uint32_t km = 0, vm = 0;
@@ -543,7 +550,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
           vm = amax_word(vm, tv[i][mt]);
         }
       }
-      done();
+      done_rows();
       const int ke = f16_exp(__reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16)));
       const int ve = f16_exp(__reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16)));
       const float kf = q8::exp2_int(-ke), vf = q8::exp2_int(-ve), ks16 = q8::exp2_int(ke);

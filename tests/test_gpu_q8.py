@@ -256,8 +256,20 @@ def test_decode_does_not_read_masked_rows():
     (2, 16, 1, 64, 130, 8, [129, 260], [8, 5]),             # 128 columns: 8 CTAs share them
     (1, 3, 1, 128, 1000, 2, [999], [2]),                    # 6 columns, clusters
     (160, 2, 1, 16, 64, 3, list(range(160)), [i % 4 for i in range(160)]),   # more pairs than SMs, some without rows
-    (2, 1, 1, 128, 200, 128, [63, 137], [128, 128]),        # the longest chunk that goes over the bytes
-    (2, 1, 1, 128, 200, 129, [63, 137], [129, 129]),        # and the shortest that does not
+    (2, 1, 1, 128, 200, 128, [63, 137], [128, 128]),        # 128 columns
+    (2, 1, 1, 128, 200, 129, [63, 137], [129, 129]),        # a ninth CTA for one column
+    # over the bytes with several rounds of each warp's ring for the chunk's own rows
+    (1, 1, 1, 16, 600, 512, [1234], [512]),
+    (1, 3, 1, 64, 700, 300, [330], [299]),
+    (2, 2, 1, 128, 520, 400, [519, 1039], [400, 337]),
+    (3, 32, 8, 16, 200, 40, [17, 0, 555], [40, 39, 3]),     # two waves
+    (3, 12, 12, 128, 130, 33, [64, 500, 129], [33, 0, 30]),
+    # written out
+    (3, 8, 8, 16, 200, 130, [17, 0, 555], [130, 129, 5]),
+    (4, 8, 4, 64, 300, 150, [299, 1, 64, 1000], [150, 128, 129, 77]),
+    (3, 16, 8, 128, 260, 77, [259, 12, 640], [77, 77, 1]),
+    (1, 1, 1, 128, 700, 513, [365], [513]),
+    (1, 4, 1, 64, 1000, 600, [2000], [600]),
 ])
 def test_prefill_matches_the_oracle(fmt, B, Hq, H, d, W, T, starts, counts):
     out = "bf16" if fmt == "int8" else "f32"
@@ -276,6 +288,29 @@ def test_prefill_matches_the_oracle(fmt, B, Hq, H, d, W, T, starts, counts):
             assert bool((o[b, n:] == 3.0).all())
             if n:
                 close(o[b, :n], want[b, :n], spread[b, :n], PREFILL_REL, 1e-6, f"sequence {b}", out)
+    same_cache(cache, ref)
+    swa.device_status()
+
+
+@pytest.mark.parametrize("pairs", [1, 14, 15, 16, 18, 19, 22, 23, 26, 27, 33, 34, 45, 46, 74, 75, 147])
+def test_pairs_in_clusters_of_every_size(pairs):
+    """From one pair in a cluster of 8 to as many as need an SM each, a decode step and a chunk."""
+    d, W, pos = 16, 64 * 64, [6000 + 37 * b for b in range(pairs)]
+    g = torch.Generator().manual_seed(pairs)
+    dims, cache, ref = make(pairs, 1, 1, d, W, "int8")
+    fill(dims, cache, ref, pos, g, W)
+    q, k, v = torch.randn(pairs, 3, 1, d, generator=g).to(torch.bfloat16), rows(g, pairs, 3, 1, d), rows(g, pairs, 3, 1, d)
+    o = torch.empty((pairs, 3, 1, d), dtype=torch.float32, device=DEV)
+    swa.prefill_chunk_q8(dims, o, q.to(DEV), k.to(DEV), v.to(DEV), cache, i32(pos), i32([3] * pairs),
+                         swa.prefill_workspace_q8(dims, 3, DEV))
+    want, spread = q8.prefill_chunk(ref, q, k, v, pos, [3] * pairs, dims.scale)
+    close(o, want, spread, DECODE_REL, W * 2.0 ** -37 * 500, "chunk")
+    o = torch.empty((pairs, 1, d), dtype=torch.float32, device=DEV)
+    q1, k1, v1 = (t[:, 0].contiguous() for t in (q, k, v))
+    swa.decode_q8(dims, o, q1.to(DEV), k1.to(DEV), v1.to(DEV), cache, i32(pos), swa.decode_workspace_q8(dims, DEV))
+    want, spread = q8.decode(ref, q1, k1, v1, pos, dims.scale)
+    # the subnormal weights' part, W 2^-37 of the largest |v| (see above)
+    close(o, want, spread, DECODE_REL, W * 2.0 ** -37 * 500, "decode")
     same_cache(cache, ref)
     swa.device_status()
 
