@@ -40,7 +40,6 @@
 // block's old rows are then all out of the window, so no CTA reads what is being written.
 #pragma once
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -205,6 +204,25 @@ constexpr int q8_smem_bytes(bool clusters) {
 __device__ __forceinline__ void cluster_begun_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
 __device__ __forceinline__ void cluster_begun_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
+// The address in CTA `rank` of the cluster of what is at `a` here.
+__device__ __forceinline__ uint32_t at_rank(uint32_t a, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+// Stores to a peer that count their bytes on its barrier when they have landed.  (Plain stores and a cluster
+// barrier: 8 pairs of 64 blocks 7.0 us and not 6.85, 2 pairs 9.7 and 8.9, 74 pairs of two CTAs 5.4 and 5.6.)
+__device__ __forceinline__ void send(uint32_t to, const float4& x, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void send(uint32_t to, const float2& x, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(x.x),
+               "f"(x.y), "r"(bar)
+               : "memory");
+}
+
 // Four elements of an output: sums against a maximum m.
 struct Four {
   float m, l;
@@ -318,9 +336,11 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   // ring of R tiles, one barrier a place, filled by TMA and freed by the warp itself
   const uint32_t ring = tc::smem_u32(smem_al) + warp * R * kTile;
   const uint32_t bars = tc::smem_u32(smem_al) + q8_ring_bytes<D, NT, NW, R>() + 16 + warp * R * 8;
+  const uint32_t peers_bar = tc::smem_u32(smem_al) + q8_ring_bytes<D, NT, NW, R>() + 8;   // all that peers send is here
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < R; ++i) tc::mbar_init(bars + 8 * i, 1);
+    if (warp == 0) tc::mbar_init(peers_bar, 1);
     tc::mbar_fence_init();
     tc::prefetch_map(&k_map);
     tc::prefetch_map(&v_map);
@@ -365,6 +385,15 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
   if (CHUNK && n_rows * G <= c0) return;             // no column of this CTA has a row
   cluster_begun_arrive();                            // waited for before the first store to a peer
+  // a cluster's CTAs merge `per` fours of the output each: theirs from every CTA, and every column's m and l
+  int n_cl = 1, rank = 0, per = 0;
+  if (p.cluster) {
+    n_cl = p.n_splits;
+    rank = split;
+    per = (cols * (D / 4) + n_cl - 1) / n_cl;
+    if (threadIdx.x == 0)
+      tc::mbar_arrive_expect_tx(peers_bar, n_cl * (16 * max(min(per, cols * (D / 4) - rank * per), 0) + 8 * cols));
+  }
   const int n_valid = pos < W ? pos + 1 : W;
   const int s_new = (int)((uint32_t)pos % (uint32_t)W);   // in 32 bits: a 64-bit remainder is a long subroutine
   const int blk0 = s_new / kQ8Block * kQ8Block;      // first slot of the block being filled
@@ -751,10 +780,6 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   __syncthreads();
 
   cluster_begun_wait();
-  namespace cg = cooperative_groups;
-  cg::cluster_group cl = cg::this_cluster();
-  const int n_cl = p.cluster ? p.n_splits : 1, rank = p.cluster ? split : 0;
-  const int per = (cols * D4 + n_cl - 1) / n_cl;     // fours that a CTA of the cluster merges
   const int live = CHUNK ? min(cols, n_rows * G - c0) : cols;   // columns with a row
   for (int idx = threadIdx.x; idx < cols * D4; idx += NW * 32) {
     const int h = idx / D4, c = idx % D4;
@@ -774,8 +799,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       if (h < live) f.store(p.out, row_of(h) * D4 + c, p.out_f32);
     } else if (CHUNK || p.cluster) {
       // each four to the CTA that merges it, m and l to all
-      cl.map_shared_rank(peer_o, idx / per)[rank * per + idx % per] = f.o;
-      for (int r = c; r < n_cl; r += D4) cl.map_shared_rank(peer_ml, r)[rank * G8 + h] = make_float2(f.m, f.l);
+      const int to = idx / per;
+      send(at_rank(tc::smem_u32(peer_o + rank * per + idx - to * per), to), f.o, at_rank(peers_bar, to));
+      for (int r = c; r < n_cl; r += D4)
+        send(at_rank(tc::smem_u32(peer_ml + rank * G8 + h), r), make_float2(f.m, f.l), at_rank(peers_bar, r));
     } else {
       const size_t part = row_of(h) * p.n_splits + split;
       reinterpret_cast<float4*>(p.ws_o)[part * D4 + c] = f.o;
@@ -784,7 +811,12 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
 
   if (p.cluster) {
-    cl.sync();   // all has been sent; every CTA of the pair's cluster comes here
+    if (!tc::mbar_wait(peers_bar, 0, p.status)) {
+      // A peer's own wait has run out (raised in the status word) and it comes late: until it has ended its
+      // stores may still arrive here.
+      asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+      tc::mbar_wait(peers_bar, 0, p.status);
+    }
     for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < live * D4; idx += NW * 32) {
       const int h = idx / D4;
       Four f;
