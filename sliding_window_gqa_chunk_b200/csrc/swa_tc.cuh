@@ -104,7 +104,8 @@ __device__ __forceinline__ void bulk_wait_read_all() {
 }
 // Waits until this thread's committed bulk stores have completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// Makes this thread's generic-proxy shared-memory writes visible to the async proxy (TMA).
+// Orders this thread's generic-proxy accesses to shared memory before later ones of the async proxy (TMA): writes
+// become visible to its reads, and reads are over before its writes.
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
