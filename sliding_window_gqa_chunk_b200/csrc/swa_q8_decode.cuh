@@ -444,8 +444,9 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   auto issue = [&]() {
     if (is_x >= r_end) return;
 #ifdef SWA_TEST_FAULTS
-    // checked build: warp 0's first tile of keys is never asked for, so its wait runs out
-    const bool withheld = p.trace != nullptr && *p.trace != 0 && warp == 0 && is_at == 0 && x0 == is_x && !is_v;
+    // checked build: warp 0's first tile of keys (2: in the first split alone) is never asked for, so its wait runs out
+    const bool withheld = p.trace != nullptr && *p.trace != 0 && (*p.trace != 2 || split == 0) && warp == 0 && is_at == 0 &&
+                          x0 == is_x && !is_v;
 #else
     constexpr bool withheld = false;
 #endif
@@ -817,14 +818,10 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     }
   }
 
+  bool late = false;
   if (p.cluster) {
-    if (!tc::mbar_wait(peers_bar, 0, p.status)) {
-      // A peer's own wait has run out (raised in the status word) and it comes late: until it has ended its
-      // stores may still arrive here.
-      asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-      tc::mbar_wait(peers_bar, 0, p.status);
-    }
-    for (int idx = rank * per + threadIdx.x; idx < (rank + 1) * per && idx < live * D4; idx += NW * 32) {
+    late = !tc::mbar_wait(peers_bar, 0, p.status);
+    for (int idx = rank * per + threadIdx.x; !late && idx < (rank + 1) * per && idx < live * D4; idx += NW * 32) {
       const int h = idx / D4;
       Four f;
       for (int r = 0; r < n_cl; ++r) f.m = fmaxf(f.m, peer_ml[r * G8 + h].x);
@@ -843,6 +840,13 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     q8::round_block<D, FMT, NW * 32>(k_row, v_row, row_new + 1, p.ring.k8 + dst, p.ring.v8 + dst,
                                      p.ring.k_scale + unit * n_blocks + blk0 / kQ8Block,
                                      p.ring.v_scale + unit * n_blocks + blk0 / kQ8Block, red);
+  }
+  if (late) {
+    // A peer's own wait has run out (raised in the status word) and it comes late: until it has ended its stores may
+    // still arrive here.  Each thread has its own verdict, so this stands behind the last barrier of the CTA: threads
+    // that saw the bytes land go on and leave, which the cluster's barrier counts as arrived.
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+    tc::mbar_wait(peers_bar, 0, p.status);
   }
 }
 
