@@ -163,7 +163,7 @@ struct Q8DecodeParams {
   const __nv_bfloat16* v_new;
   const int32_t* pos;           // device [B]
   float* ws_o;                  // [B][Hq][n_splits][d] partial O (two launches)
-  float* ws_ml;                 // [B][Hq][n_splits][2] partial (max, sum)
+  float* ws_ml;                 // [B][Hq][n_splits][4] partial (max, score of the sum, sum, 0)
   int* status;
   const int32_t* n_tokens;      // device [B], or NULL: one token, which is taken in
   int max_tokens, groups;       // rows of a chunk, CTAs that share its columns

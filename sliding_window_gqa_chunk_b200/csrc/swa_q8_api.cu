@@ -192,7 +192,7 @@ size_t swa_q8_decode_workspace_size(const swa_dims* dims) {
   if (check_q8_dims(dims) != SWA_OK) return 0;
   const swa::Q8DecodeSplit sp = split_of(dims, 1, false);
   if (sp.n_splits == 1 || sp.cluster) return 16;  // nothing needed; a non-zero size keeps callers simple
-  return (size_t)dims->batch * dims->n_q_heads * sp.n_splits * (dims->head_dim + 2) * sizeof(float);
+  return (size_t)dims->batch * dims->n_q_heads * sp.n_splits * (dims->head_dim + 4) * sizeof(float);
 }
 
 int swa_q8_decode(const swa_dims* dims, void* out, const void* q, const void* k_new, const void* v_new,

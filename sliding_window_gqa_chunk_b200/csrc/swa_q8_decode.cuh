@@ -19,8 +19,10 @@
 // w = 2^(x + v - m + 15), where the running m is the maximum of x + v rather than of x.
 // The numbers of a block's values always reach the top of their format, so w orders the
 // slots by what they can add to the output and is at most 2^15: f16 keeps 11 bits of the
-// weights down to 2^-29 of the largest.  The softmax sum is that of 2^(x - m) =
-// w 2^(-v - 15), in fp32.  Q goes to f16 with one power of two for each head (its largest
+// weights down to 2^-29 of the largest.  The softmax sum is that of 2^(x - r), in fp32, against
+// a score r of its own: the first block's largest, 2^40 of which may pass before it moves.  It is
+// taken from the weights, w 2^(m - v - 15 - r), but where these have lost it (m above x + v by
+// more than 2^55: values of very different sizes), from the scores.  Q goes to f16 with one power of two for each head (its largest
 // magnitude to [2^14, 2^15)): its 8 bits are kept in all elements above 2^-28 of the
 // largest.  The rows of the block being filled (at most 64, in bf16) go through the same
 // products, 16 rows with a power of two of their own at a time.
@@ -33,7 +35,7 @@
 // 12 KB for 16 warps 100 us (the arithmetic of a block is as long as a ring).
 //
 // Work split: grid (n_splits, Hkv, B); the warps of a CTA take the 64-slot blocks of its split
-// in turn and merge their (m, l, O) in shared memory, and the splits of a pair merge through
+// in turn and merge their (m, r, l, O) in shared memory, and the splits of a pair merge through
 // distributed shared memory (thread-block cluster) or through the workspace and a second
 // kernel.  The CTA whose split holds slot pos mod W takes the rows of the tail into its sweep,
 // writes the new row there or, if it is its block's last, rounds the block into the ring.  That
@@ -180,14 +182,14 @@ __device__ __forceinline__ int f16_exp(uint32_t amax) {
   return e < -126 ? -126 : (e > 113 ? 113 : e);
 }
 
-// Shared memory of the merge: m, l and O of each warp (in the rings, once every warp is
+// Shared memory of the merge: (m, r, l) and O of each warp (in the rings, once every warp is
 // done with its own), and what the CTAs of a cluster send to one another.
 template <int D, int NT, int NW>
 constexpr int q8_merge_bytes() {
-  return (int)sizeof(float) * NW * 8 * NT * (2 + D);
+  return (int)sizeof(float) * NW * 8 * NT * (4 + D);
 }
 template <int D, int NT>
-constexpr int q8_peer_floats() { return kMaxCluster * 8 * NT * 2 + 8 * NT * D + 4 * kMaxCluster; }
+constexpr int q8_peer_floats() { return kMaxCluster * 8 * NT * 4 + 8 * NT * D + 4 * kMaxCluster; }
 template <int D, int NT, int NW, int R>
 constexpr int q8_ring_bytes() {
   constexpr int ring = NW * R * kQ8Block * D, merge = q8_merge_bytes<D, NT, NW>();
@@ -217,28 +219,31 @@ __device__ __forceinline__ void send(uint32_t to, const float4& x, uint32_t bar)
                "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void send(uint32_t to, const float2& x, uint32_t bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(x.x),
-               "f"(x.y), "r"(bar)
-               : "memory");
-}
 
-// Four elements of an output: sums against a maximum m.
+// Four elements of an output: o against m, the largest score and value scale, l against the score r.
+// A part is (m, r, l) and its o; one without rows is (-inf, -inf, 0).
 struct Four {
-  float m, l;
+  float m, r, l;
   float4 o;
-  __device__ __forceinline__ Four() : m(-INFINITY), l(0.f), o(make_float4(0.f, 0.f, 0.f, 0.f)) {}
-  __device__ __forceinline__ void add(float s, float l2, const float4& o2) {
-    l += s * l2;
+  __device__ __forceinline__ Four() : m(-INFINITY), r(-INFINITY), l(0.f), o(make_float4(0.f, 0.f, 0.f, 0.f)) {}
+  __device__ __forceinline__ void against(const float4& part) {
+    m = fmaxf(m, part.x);
+    r = fmaxf(r, part.y);
+  }
+  __device__ __forceinline__ void add(const float4& part, const float4& o2) {
+    const float s = fast_exp2(part.x - m);
+    l += fast_exp2(part.y - r) * part.z;
     o.x += s * o2.x;
     o.y += s * o2.y;
     o.z += s * o2.z;
     o.w += s * o2.w;
   }
-  // the i-th four of the output; weights are in units of kWeightUnit, their sum is not
+  // the i-th four of the output; weights are in units of kWeightUnit, their sum is not.  2^(m - r) in two
+  // halves: it may leave fp32's range where the output does not.
   __device__ __forceinline__ void store(void* out, size_t i, int f32) const {
-    const float x = o.x * kWeightUnit / l, y = o.y * kWeightUnit / l;
-    const float z = o.z * kWeightUnit / l, w = o.w * kWeightUnit / l;
+    const float h = fast_exp2(0.5f * (m - r));
+    const float x = o.x * kWeightUnit / l * h * h, y = o.y * kWeightUnit / l * h * h;
+    const float z = o.z * kWeightUnit / l * h * h, w = o.w * kWeightUnit / l * h * h;
     if (f32) reinterpret_cast<float4*>(out)[i] = make_float4(x, y, z, w);
     else reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
   }
@@ -249,7 +254,7 @@ struct Four {
 // g D / 8 + 2 mt and the next one.
 template <int D>
 struct State {
-  float m[2], l[2];
+  float m[2], r[2], l[2];
   float o[Q8Frag<D>::kMTiles][4];
 };
 
@@ -257,12 +262,16 @@ struct State {
 // where a masked -inf stays -inf and a dot product of 0 stays 0.
 __device__ __forceinline__ float score_factor(float q, float k) { return fminf(fmaxf(q * k, 1e-37f), 1e37f); }
 
+// Where the sum's terms leave the range in which they are taken from the weights: log2 of the largest
+// against the sum's r, and of the factor from a weight to its term.
+constexpr float kFar = 40.f;
+
 // Dot products `x` (-inf where masked) of SUB blocks of 16 slots, to be multiplied
 // by f0, f1 (> 0, finite; heads 2t, 2t + 1) for scores in log2 units, with the value
-// scale 2^v -> weights as B fragments; updates m, l and rescales O.
+// scale 2^v -> weights as B fragments; updates m, r, l and rescales O.
 // GUARD: a column may have no unmasked row (else every one has).
 template <int D, int SUB, bool GUARD>
-__device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB][4], float f0, float f1, int v,
+__device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB][4], float f0, float f1, float v,
                                              uint32_t (&pb)[SUB][2]) {
   float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
 #pragma unroll
@@ -275,14 +284,42 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
   }
-  const float fv = (float)v, inv = q8::exp2_int(-v);
-  const float n0 = fmaxf(st.m[0], fmaf(mx0, f0, fv)), n1 = fmaxf(st.m[1], fmaf(mx1, f1, fv));
   // where nothing has been seen yet, exponents are taken against 0: all of them are of -inf
-  const float b0 = GUARD && n0 == -CUDART_INF_F ? 0.f : n0, b1 = GUARD && n1 == -CUDART_INF_F ? 0.f : n1;
-  const float a0 = fast_exp2(st.m[0] - b0), a1 = fast_exp2(st.m[1] - b1);
+  auto base = [](float n) { return GUARD && n == -CUDART_INF_F ? 0.f : n; };
+  const float y0 = mx0 * f0, y1 = mx1 * f1;
+  const float n0 = fmaxf(st.m[0], fmaf(mx0, f0, v)), n1 = fmaxf(st.m[1], fmaf(mx1, f1, v));
+  const float a0 = fast_exp2(st.m[0] - base(n0)), a1 = fast_exp2(st.m[1] - base(n1));
   st.m[0] = n0;
   st.m[1] = n1;
-  const float c0 = fv + kWeightExp - b0, c1 = fv + kWeightExp - b1;
+  const float c0 = v + kWeightExp - base(n0), c1 = v + kWeightExp - base(n1);
+  if (st.r[0] == -CUDART_INF_F) st.r[0] = y0;
+  if (st.r[1] == -CUDART_INF_F) st.r[1] = y1;
+  // from a weight to its term of the sum
+  float e0 = -c0 - base(st.r[0]), e1 = -c1 - base(st.r[1]);
+  const bool far = fmaxf(fmaxf(y0 - st.r[0], e0), fmaxf(y1 - st.r[1], e1)) > kFar;
+  if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f || far)) {   // a maximum moved
+#pragma unroll
+    for (int mt = 0; mt < Q8Frag<D>::kMTiles; ++mt) {
+      st.o[mt][0] *= a0;
+      st.o[mt][1] *= a1;
+      st.o[mt][2] *= a0;
+      st.o[mt][3] *= a1;
+    }
+    if (__any_sync(0xffffffffu, far)) {
+      const float r0 = fmaxf(st.r[0], y0), r1 = fmaxf(st.r[1], y1);
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        s0 += fast_exp2(fmaf(x[u][0], f0, -base(r0))) + fast_exp2(fmaf(x[u][2], f0, -base(r0)));
+        s1 += fast_exp2(fmaf(x[u][1], f1, -base(r1))) + fast_exp2(fmaf(x[u][3], f1, -base(r1)));
+      }
+      st.l[0] = st.l[0] * fast_exp2(st.r[0] - base(r0)) + s0;
+      st.l[1] = st.l[1] * fast_exp2(st.r[1] - base(r1)) + s1;
+      st.r[0] = r0;
+      st.r[1] = r1;
+      e0 = e1 = -CUDART_INF_F;
+    }
+  }
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
@@ -293,17 +330,8 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
     pb[u][0] = movmatrix_trans(pack_f16x2(p0, p1));
     pb[u][1] = movmatrix_trans(pack_f16x2(p2, p3));
   }
-  st.l[0] = st.l[0] * a0 + s0 * kWeightUnit * inv;
-  st.l[1] = st.l[1] * a1 + s1 * kWeightUnit * inv;
-  if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {   // a maximum moved
-#pragma unroll
-    for (int mt = 0; mt < Q8Frag<D>::kMTiles; ++mt) {
-      st.o[mt][0] *= a0;
-      st.o[mt][1] *= a1;
-      st.o[mt][2] *= a0;
-      st.o[mt][3] *= a1;
-    }
-  }
+  st.l[0] += s0 * fast_exp2(e0);
+  st.l[1] += s1 * fast_exp2(e1);
 }
 
 }  // namespace
@@ -385,14 +413,14 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
   if (CHUNK && n_rows * G <= c0) return;             // no column of this CTA has a row
   cluster_begun_arrive();                            // waited for before the first store to a peer
-  // a cluster's CTAs merge `per` fours of the output each: theirs from every CTA, and every column's m and l
+  // a cluster's CTAs merge `per` fours of the output each: theirs from every CTA, and every column's (m, r, l)
   int n_cl = 1, rank = 0, per = 0;
   if (p.cluster) {
     n_cl = p.n_splits;
     rank = split;
     per = (cols * (D / 4) + n_cl - 1) / n_cl;
     if (threadIdx.x == 0)
-      tc::mbar_arrive_expect_tx(peers_bar, n_cl * (16 * max(min(per, cols * (D / 4) - rank * per), 0) + 8 * cols));
+      tc::mbar_arrive_expect_tx(peers_bar, n_cl * 16 * (max(min(per, cols * (D / 4) - rank * per), 0) + cols));
   }
   const int n_valid = pos < W ? pos + 1 : W;
   const int s_new = (int)((uint32_t)pos % (uint32_t)W);   // in 32 bits: a 64-bit remainder is a long subroutine
@@ -525,7 +553,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   State<D> st[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    st[nt].m[0] = st[nt].m[1] = -CUDART_INF_F;
+    st[nt].m[0] = st[nt].m[1] = st[nt].r[0] = st[nt].r[1] = -CUDART_INF_F;
     st[nt].l[0] = st[nt].l[1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < F::kMTiles; ++mt) st[nt].o[mt][0] = st[nt].o[mt][1] = st[nt].o[mt][2] = st[nt].o[mt][3] = 0.f;
@@ -621,7 +649,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
           if (!see1) x[0][2 + c] = -CUDART_INF_F;
         }
         uint32_t pb[1][2];
-        softmax_step<D, 1, CHUNK>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), ve, pb);
+        softmax_step<D, 1, CHUNK>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), (float)ve, pb);
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt)
           mma_f16(st[nt].o[mt], prmt(tv[0][mt], tv[1][mt], 0x5410), prmt(tv[0][mt], tv[1][mt], 0x7632),
@@ -700,8 +728,8 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      softmax_step<D, kSubs, CHUNK>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks), q8::exp_of(vs),
-                             pb[nt]);
+      softmax_step<D, kSubs, CHUNK>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks),
+                                    (float)q8::exp_of(vs), pb[nt]);
 
     tile = take();
     if (!ok) break;
@@ -752,16 +780,16 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
 
   // ---- merge the NW warps of the CTA ----
-  // in the rings, once every warp is done with its own: (m, l)[NW][G8], then O[NW][G8][D] with the
+  // in the rings, once every warp is done with its own: (m, r, l)[NW][G8], then O[NW][G8][D] with the
   // c-th four of a column h at c ^ (h / 2 & 3), so that the four columns of a store fall on different banks
   __syncthreads();
   constexpr int G8 = 8 * NT, D4 = D / 4;
-  float2* sm_ml = reinterpret_cast<float2*>(smem_al);
-  float4* sm_o = reinterpret_cast<float4*>(sm_ml + NW * G8);
+  float4* sm_ml = reinterpret_cast<float4*>(smem_al);
+  float4* sm_o = sm_ml + NW * G8;
   uint32_t* red = reinterpret_cast<uint32_t*>(smem_al + q8_ring_bytes<D, NT, NW, R>());
-  // what the peers of a cluster send: O[rank][share], then (m, l)[rank][G8]
+  // what the peers of a cluster send: O[rank][share], then (m, r, l)[rank][G8]
   float4* peer_o = reinterpret_cast<float4*>(smem_al + q8_ring_bytes<D, NT, NW, R>() + 16 + NW * R * 8);
-  float2* peer_ml = reinterpret_cast<float2*>(peer_o + G8 * D4 + kMaxCluster);
+  float4* peer_ml = peer_o + G8 * D4 + kMaxCluster;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float l0 = st[nt].l[0], l1 = st[nt].l[1];
@@ -773,7 +801,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int h = nt * 8 + 2 * t + e;
-      if (g == 0) sm_ml[warp * G8 + h] = make_float2(st[nt].m[e], e ? l1 : l0);
+      if (g == 0) sm_ml[warp * G8 + h] = make_float4(st[nt].m[e], st[nt].r[e], e ? l1 : l0, 0.f);
       float4* o = sm_o + (warp * G8 + h) * D4;
       if constexpr (D == 16) {                 // two elements a lane
         reinterpret_cast<float2*>(o)[2 * ((g / 2) ^ t) + (g & 1)] = make_float2(st[nt].o[0][e], st[nt].o[0][2 + e]);
@@ -792,29 +820,28 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   for (int idx = threadIdx.x; idx < cols * D4; idx += NW * 32) {
     const int h = idx / D4, c = idx % D4;
     Four f;
-    float2 ml[NW];
+    float4 ml[NW];
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       ml[w] = sm_ml[w * G8 + h];
-      f.m = fmaxf(f.m, ml[w].x);
+      f.against(ml[w]);
     }
     if (f.m != -CUDART_INF_F) {
 #pragma unroll
-      for (int w = 0; w < NW; ++w)
-        f.add(fast_exp2(ml[w].x - f.m), ml[w].y, sm_o[(w * G8 + h) * D4 + (c ^ (h / 2 & 3))]);
+      for (int w = 0; w < NW; ++w) f.add(ml[w], sm_o[(w * G8 + h) * D4 + (c ^ (h / 2 & 3))]);
     }
     if (p.n_splits == 1) {
       if (h < live) f.store(p.out, row_of(h) * D4 + c, p.out_f32);
     } else if (CHUNK || p.cluster) {
-      // each four to the CTA that merges it, m and l to all
+      // each four to the CTA that merges it, (m, r, l) to all
       const int to = idx / per;
       send(at_rank(tc::smem_u32(peer_o + rank * per + idx - to * per), to), f.o, at_rank(peers_bar, to));
       for (int r = c; r < n_cl; r += D4)
-        send(at_rank(tc::smem_u32(peer_ml + rank * G8 + h), r), make_float2(f.m, f.l), at_rank(peers_bar, r));
+        send(at_rank(tc::smem_u32(peer_ml + rank * G8 + h), r), make_float4(f.m, f.r, f.l, 0.f), at_rank(peers_bar, r));
     } else {
       const size_t part = row_of(h) * p.n_splits + split;
       reinterpret_cast<float4*>(p.ws_o)[part * D4 + c] = f.o;
-      if (c == 0) reinterpret_cast<float2*>(p.ws_ml)[part] = make_float2(f.m, f.l);
+      if (c == 0) reinterpret_cast<float4*>(p.ws_ml)[part] = make_float4(f.m, f.r, f.l, 0.f);
     }
   }
 
@@ -824,11 +851,8 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
     for (int idx = rank * per + threadIdx.x; !late && idx < (rank + 1) * per && idx < live * D4; idx += NW * 32) {
       const int h = idx / D4;
       Four f;
-      for (int r = 0; r < n_cl; ++r) f.m = fmaxf(f.m, peer_ml[r * G8 + h].x);
-      for (int r = 0; r < n_cl; ++r) {
-        const float2 ml = peer_ml[r * G8 + h];
-        f.add(fast_exp2(ml.x - f.m), ml.y, peer_o[r * per + idx - rank * per]);
-      }
+      for (int r = 0; r < n_cl; ++r) f.against(peer_ml[r * G8 + h]);
+      for (int r = 0; r < n_cl; ++r) f.add(peer_ml[r * G8 + h], peer_o[r * per + idx - rank * per]);
       f.store(p.out, row_of(h) * D4 + idx % D4, p.out_f32);
     }
   }
@@ -859,13 +883,13 @@ __global__ void __launch_bounds__(32) swa_q8_decode_combine_kernel(const Q8Decod
   const int c = threadIdx.x;
   if (c >= D / 4 || p.pos[bh / p.n_q_heads] < 0) return;
   const int S = p.n_splits;
-  const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + bh * S;
+  const float4* ml = reinterpret_cast<const float4*>(p.ws_ml) + bh * S;
   const float4* o = reinterpret_cast<const float4*>(p.ws_o) + bh * S * (D / 4) + c;
   Four f;
 #pragma unroll 8
-  for (int s = 0; s < S; ++s) f.m = fmaxf(f.m, ml[s].x);
+  for (int s = 0; s < S; ++s) f.against(ml[s]);
 #pragma unroll 8
-  for (int s = 0; s < S; ++s) f.add(fast_exp2(ml[s].x - f.m), ml[s].y, o[(size_t)s * (D / 4)]);
+  for (int s = 0; s < S; ++s) f.add(ml[s], o[(size_t)s * (D / 4)]);
   f.store(p.out, bh * (D / 4) + c, p.out_f32);
 }
 

@@ -1,0 +1,114 @@
+"""The 8-bit cache's decode steps and few-row chunks where values of one window differ in size, against
+the float64 oracle (oracle/q8.py).
+
+A weight is held in f16, 2^15 for the row with the largest product p* of softmax weight and value scale: it is off by
+2^-11 of itself or, below 2^-14, by 2^-25.  The scores (d products, sizes below 2^4), exp2 and the fp32 sums stay within
+another 2^-11.  With S the weighted mean of |v| the first and the last make 2^-10 S.  The second is 2^-40 of p* for each
+of n rows, times a number of at most 2^15 where that row's scale makes its largest number 2^6 at least: n 2^-31 of the
+row's weight times its largest |v|.  Rows here are at least half as large everywhere as in one place, so that is at most
+n 2^-30 S, and with n <= 2^16 it stays below 2^-14 S."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import sliding_window_gqa_chunk_b200 as swa
+from oracle import q8
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+REL = 2.0 ** -10 + 2.0 ** -14
+
+
+def i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device=DEV)
+
+
+def bf16(x):
+    return x.to(torch.bfloat16)
+
+
+def close(got, want, spread, what):
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all(), what
+    # below fp32's normal numbers an output keeps 2^-150
+    worst = float((np.abs(got - want) / (REL * spread + 2.0 ** -149)).max())
+    assert worst <= 1.0, f"{what}: {worst:.3g} of the bound"
+
+
+# largest sizes of the values of a ring's blocks, in turn (block j: sizes[j % len]).  Of odd length,
+# so that a warp, which takes every eighth or fourth block, meets all of them.
+SIZES = {
+    "2^100 and 2^-60": [2.0 ** 100, 2.0 ** -60, 2.0 ** -60],
+    "2^-60 and 2^100": [2.0 ** -60, 2.0 ** -60, 2.0 ** 100],
+    "2^-112": [2.0 ** -112],
+}
+# B, Hq, H, d, W, first position: warps of one CTA with a block each; a short sequence in the tail alone; several blocks
+# to each warp of a cluster of 8, with the open block's old rows; several to a warp of a pair's only CTA
+SHAPES = [
+    (2, 4, 1, 128, 256, 700),
+    (1, 4, 1, 64, 150 * 64, 38),
+    (1, 12, 1, 128, 140 * 64, 141 * 64 + 37),
+    (1, 3, 1, 64, 150 * 64 - 5, 160 * 64),
+    (150, 1, 1, 16, 320, 333),
+]
+
+
+def run(dims, cache, ref, q, k, v, pos, T):
+    """A chunk of T rows, then its first row as a decode step; both against the oracle."""
+    B, Hq, d = dims.batch, dims.n_q_heads, dims.head_dim
+    o = torch.full((B, T, Hq, d), float("nan"), device=DEV)
+    swa.prefill_chunk_q8(dims, o, q.to(DEV), k.to(DEV), v.to(DEV), cache, i32(pos), i32([T] * B),
+                         swa.prefill_workspace_q8(dims, T, DEV))
+    want, spread = q8.prefill_chunk(ref, q, k, v, pos, [T] * B, dims.scale)
+    close(o, want, spread, "chunk")
+    o = torch.full((B, Hq, d), float("nan"), device=DEV)
+    q1, k1, v1 = (x[:, 0].contiguous() for x in (q, k, v))
+    swa.decode_q8(dims, o, q1.to(DEV), k1.to(DEV), v1.to(DEV), cache, i32(pos), swa.decode_workspace_q8(dims, DEV))
+    want, spread = q8.decode(ref, q1, k1, v1, pos, dims.scale)
+    close(o, want, spread, "decode step")
+    swa.device_status()
+
+
+def sized(g, sizes, B, n, H, d, W, start=0):
+    """Values of rows start .. start + n - 1, each of its block's size."""
+    at = (start + torch.arange(n)) % W // q8.BLOCK
+    size = torch.tensor(sizes, dtype=torch.float64)[at % len(sizes)].view(1, n, 1, 1)
+    sign = torch.randint(0, 2, (B, n, H, d), generator=g) * 2 - 1
+    return bf16((torch.rand(B, n, H, d, generator=g) * 0.5 + 0.5) * sign * size)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,Hq,H,d,W,pos", SHAPES)
+@pytest.mark.parametrize("name", list(SIZES))
+def test_blocks_of_far_sizes(name, B, Hq, H, d, W, pos, fmt):
+    sizes = SIZES[name]
+    if name == "2^-112":
+        pos = min(pos, 63)             # what is in the tail: a ring's scale is 2^-100 at least
+    g = torch.Generator().manual_seed(W + d)
+    dims = swa.Dims(B, Hq, H, d, W, 1.0 / math.sqrt(d), "f32")
+    cache, ref = swa.new_cache_q8(dims, fmt, DEV), q8.RollingCacheQ8(B, H, W, d, fmt)
+    for s in range(0, pos, 4096 if W > 4096 else W):
+        n = min(4096, W, pos - s)
+        k, v = bf16(torch.randn(B, n, H, d, generator=g)), sized(g, sizes, B, n, H, d, W, s)
+        swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([s] * B), i32([n] * B))
+        q8.append(ref, k, v, [s] * B, [n] * B)
+    T = 3
+    run(dims, cache, ref, bf16(torch.randn(B, T, Hq, d, generator=g)), bf16(torch.randn(B, T, H, d, generator=g)),
+        sized(g, sizes, B, T, H, d, W, pos), [pos] * B, T)
+
+
+@pytest.mark.parametrize("sizes", [[2.0 ** 100, 2.0 ** -60, 2.0 ** -60], [1.0, 16.0, 1.0]])
+def test_far_sizes_over_all_sms(sizes):
+    """A window whose partial results are merged by a second kernel."""
+    B, Hq, H, d, W = 1, 4, 1, 16, 1900 * 64
+    g = torch.Generator().manual_seed(5)
+    dims = swa.Dims(B, Hq, H, d, W, 0.25, "f32")
+    assert swa.decode_workspace_size_q8(dims) > 16
+    cache, ref = swa.new_cache_q8(dims, "int8", DEV), q8.RollingCacheQ8(B, H, W, d, "int8")
+    k, v = bf16(torch.randn(B, W, H, d, generator=g)), sized(g, sizes, B, W, H, d, W)
+    swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([0]), i32([W]))
+    q8.append(ref, k, v, [0], [W])
+    q, k1 = bf16(torch.randn(B, 1, Hq, d, generator=g)), bf16(torch.randn(B, 1, H, d, generator=g))
+    run(dims, cache, ref, q, k1, sized(g, sizes, B, 1, H, d, W), [W], 1)
