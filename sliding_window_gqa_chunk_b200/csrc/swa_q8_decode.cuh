@@ -17,12 +17,14 @@
 // Scales.  A block's key scale multiplies its scores.  Its value scale 2^v is put into
 // the exponent of the softmax: with x the score in log2 units, the weight of a slot is
 // w = 2^(x + v - m + 15), where the running m is the maximum of x + v rather than of x.
-// The numbers of a block's values always reach the top of their format, so w orders the
+// The numbers of a block's values reach the top of their format, so w orders the
 // slots by what they can add to the output and is at most 2^15: f16 keeps 11 bits of the
 // weights down to 2^-29 of the largest.  The softmax sum is that of 2^(x - r), in fp32, against
 // a score r of its own: the first block's largest, 2^40 of which may pass before it moves.  It is
 // taken from the weights, w 2^(m - v - 15 - r), but where these have lost it (m above x + v by
-// more than 2^55: values of very different sizes), from the scores.  Q goes to f16 with one power of two for each head (its largest
+// more than 2^55: values of very different sizes), from the scores.  A block of zeros has a scale
+// of 1 that says nothing of its size: it is told from others of that scale by its bytes, and, as
+// zero rows in bf16, takes a scale below all others, which moves no m.  Q goes to f16 with one power of two for each head (its largest
 // magnitude to [2^14, 2^15)): its 8 bits are kept in all elements above 2^-28 of the
 // largest.  The rows of the block being filled (at most 64, in bf16) go through the same
 // products, 16 rows with a power of two of their own at a time.
@@ -144,6 +146,18 @@ __device__ __forceinline__ void load_val8(uint32_t (&w)[Q8Frag<D>::kVWords], uin
   }
 }
 
+// Whether rows [lo, hi) of a tile hold nothing but zeros.  (A call, so that the registers it takes are not
+// those of the loop it is called from, where blocks of zeros are rare.)
+template <int D, int FMT>
+__device__ __noinline__ bool all_zero(uint32_t tile, int lo, int hi) {
+  uint32_t any = 0;
+  for (int i = lo * D + 4 * (int)(threadIdx.x & 31); i < hi * D; i += 4 * 32) {
+    const uint32_t x = lds32(tile + i);        // the swizzle moves pieces within a row
+    any |= FMT == SWA_Q8_E4M3 ? x & 0x7f7f7f7fu : x;
+  }
+  return !__any_sync(0xffffffffu, any != 0);
+}
+
 // D += A * B for one 16x8x16 f16 tile, fp32 accumulators (warp-wide).
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -175,6 +189,9 @@ __device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w, float s) {
   return pack_f16x2(q8::bf16_lo(w) * s, q8::bf16_hi(w) * s);
 }
 __device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+// Exponent of the value scale of zeros: below that of all others by more than scores differ.
+constexpr float kZeroExp = -1000.f;
+
 // Exponent that brings a largest magnitude (bf16 bits) to [2^14, 2^15): x 2^-e.
 __device__ __forceinline__ int f16_exp(uint32_t amax) {
   if (amax == 0) return 0;
@@ -617,7 +634,9 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       }
       done_rows();
       const int ke = f16_exp(__reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16)));
-      const int ve = f16_exp(__reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16)));
+      vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
+      const int ve = f16_exp(vm);
+      const float vsize = vm == 0 ? kZeroExp : (float)ve;
       const float kf = q8::exp2_int(-ke), vf = q8::exp2_int(-ve), ks16 = q8::exp2_int(ke);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -649,7 +668,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
           if (!see1) x[0][2 + c] = -CUDART_INF_F;
         }
         uint32_t pb[1][2];
-        softmax_step<D, 1, CHUNK>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), (float)ve, pb);
+        softmax_step<D, 1, CHUNK>(st[nt], x, score_factor(qs[nt][0], ks16), score_factor(qs[nt][1], ks16), vsize, pb);
 #pragma unroll
         for (int mt = 0; mt < F::kMTiles; ++mt)
           mma_f16(st[nt].o[mt], prmt(tv[0][mt], tv[1][mt], 0x5410), prmt(tv[0][mt], tv[1][mt], 0x7632),
@@ -696,6 +715,11 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       }
     }
 
+    tile = take();
+    if (!ok) break;
+    float vsize = (float)q8::exp_of(vs);
+    // a block of zeros, or one that needs no scale: its bytes tell
+    if (vs == 1.f && all_zero<D, FMT>(tile, lo - x0, hi - x0)) vsize = kZeroExp;
     uint32_t pb[NT][kSubs][2];
     if constexpr (CHUNK) {
       // the slot a places after s_new (round the ring) holds position start - W + a: seen by rows below a
@@ -729,10 +753,8 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
       softmax_step<D, kSubs, CHUNK>(st[nt], x[nt], score_factor(qs[nt][0], ks), score_factor(qs[nt][1], ks),
-                                    (float)q8::exp_of(vs), pb[nt]);
+                                    vsize, pb[nt]);
 
-    tile = take();
-    if (!ok) break;
 #pragma unroll
     for (int u = 0; u < kSubs; u += 2) {
       uint32_t vw[2][4][F::kVWords];

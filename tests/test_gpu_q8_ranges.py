@@ -1,4 +1,4 @@
-"""The 8-bit cache's decode steps and few-row chunks where values of one window differ in size, against
+"""The 8-bit cache's decode steps and few-row chunks where values of one window differ in size, or are zero, against
 the float64 oracle (oracle/q8.py).
 
 A weight is held in f16, 2^15 for the row with the largest product p* of softmax weight and value scale: it is off by
@@ -6,7 +6,8 @@ A weight is held in f16, 2^15 for the row with the largest product p* of softmax
 another 2^-11.  With S the weighted mean of |v| the first and the last make 2^-10 S.  The second is 2^-40 of p* for each
 of n rows, times a number of at most 2^15 where that row's scale makes its largest number 2^6 at least: n 2^-31 of the
 row's weight times its largest |v|.  Rows here are at least half as large everywhere as in one place, so that is at most
-n 2^-30 S, and with n <= 2^16 it stays below 2^-14 S."""
+n 2^-30 S; a row of zeros among others in a ring's block may weigh more than they do by its score, 2^9 at most.  With
+n <= 2^16 / 2^9 there and n <= 2^16 elsewhere it stays below 2^-14 S."""
 import math
 
 import numpy as np
@@ -37,12 +38,19 @@ def close(got, want, spread, what):
     assert worst <= 1.0, f"{what}: {worst:.3g} of the bound"
 
 
-# largest sizes of the values of a ring's blocks, in turn (block j: sizes[j % len]).  Of odd length,
+# largest sizes of the values of a ring's blocks, in turn (block j: sizes[j % len]); 0: a block of zeros.  Of odd length,
 # so that a warp, which takes every eighth or fourth block, meets all of them.
 SIZES = {
+    "zeros beside 2^-24": [0.0, 2.0 ** -24, 2.0 ** -24],
+    "zeros beside 2^-36, 2^-30": [2.0 ** -36, 0.0, 2.0 ** -30],
+    "zeros beside 2^-80": [2.0 ** -80, 2.0 ** -80, 0.0],
+    "zeros alone": [0.0],
+    "zeros beside 2^100": [0.0, 0.0, 2.0 ** 100],
     "2^100 and 2^-60": [2.0 ** 100, 2.0 ** -60, 2.0 ** -60],
     "2^-60 and 2^100": [2.0 ** -60, 2.0 ** -60, 2.0 ** 100],
+    "2^-60, zeros and 2^100": [2.0 ** -60, 0.0, 2.0 ** 100],
     "2^-112": [2.0 ** -112],
+    "1, zeros and 300": [1.0, 0.0, 300.0],         # a scale of 1 that is not of zeros (e4m3; int8: 100)
 }
 # B, Hq, H, d, W, first position: warps of one CTA with a block each; a short sequence in the tail alone; several blocks
 # to each warp of a cluster of 8, with the open block's old rows; several to a warp of a pair's only CTA
@@ -83,7 +91,7 @@ def sized(g, sizes, B, n, H, d, W, start=0):
 @pytest.mark.parametrize("B,Hq,H,d,W,pos", SHAPES)
 @pytest.mark.parametrize("name", list(SIZES))
 def test_blocks_of_far_sizes(name, B, Hq, H, d, W, pos, fmt):
-    sizes = SIZES[name]
+    sizes = [min(s, 100.0) if s > 1 and s < 2.0 ** 10 and fmt == "int8" else s for s in SIZES[name]]
     if name == "2^-112":
         pos = min(pos, 63)             # what is in the tail: a ring's scale is 2^-100 at least
     g = torch.Generator().manual_seed(W + d)
@@ -99,7 +107,25 @@ def test_blocks_of_far_sizes(name, B, Hq, H, d, W, pos, fmt):
         sized(g, sizes, B, T, H, d, W, pos), [pos] * B, T)
 
 
-@pytest.mark.parametrize("sizes", [[2.0 ** 100, 2.0 ** -60, 2.0 ** -60], [1.0, 16.0, 1.0]])
+@pytest.mark.parametrize("size", [2.0 ** -28, 2.0 ** 60])
+def test_zero_rows_of_the_tail_and_of_the_chunk(size):
+    """16 rows of zeros in the block being filled, in the ring's blocks none, and a new row of zeros."""
+    B, Hq, H, d, W, pos = 2, 8, 2, 64, 256, 512 + 60
+    g = torch.Generator().manual_seed(3)
+    dims = swa.Dims(B, Hq, H, d, W, 0.125, "f32")
+    cache, ref = swa.new_cache_q8(dims, "e4m3", DEV), q8.RollingCacheQ8(B, H, W, d, "e4m3")
+    for s in range(0, pos, 128):
+        n = min(128, pos - s)
+        k, v = bf16(torch.randn(B, n, H, d, generator=g)), sized(g, [size], B, n, H, d, W)
+        if s + n == pos:
+            v[:, n - 44:n - 12] = 0.0      # rows 16 .. 47 of the open block
+        swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([s] * B), i32([n] * B))
+        q8.append(ref, k, v, [s] * B, [n] * B)
+    q, k = bf16(torch.randn(B, 2, Hq, d, generator=g)), bf16(torch.randn(B, 2, H, d, generator=g))
+    run(dims, cache, ref, q, k, torch.zeros(B, 2, H, d, dtype=torch.bfloat16), [pos] * B, 2)
+
+
+@pytest.mark.parametrize("sizes", [[2.0 ** 100, 2.0 ** -60, 2.0 ** -60], [1.0, 16.0, 1.0], [0.0, 2.0 ** -30, 2.0 ** -30]])
 def test_far_sizes_over_all_sms(sizes):
     """A window whose partial results are merged by a second kernel."""
     B, Hq, H, d, W = 1, 4, 1, 16, 1900 * 64
