@@ -138,3 +138,47 @@ def test_far_sizes_over_all_sms(sizes):
     q8.append(ref, k, v, [0], [W])
     q, k1 = bf16(torch.randn(B, 1, Hq, d, generator=g)), bf16(torch.randn(B, 1, H, d, generator=g))
     run(dims, cache, ref, q, k1, sized(g, sizes, B, 1, H, d, W), [W], 1)
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("pos", [0, 16, 256 + 19])
+def test_rows_of_a_chunk_do_not_see_the_sizes_of_later_ones(pos, fmt):
+    """Rows whose keys or values are 2^40 times those of the rows before them, in one group of 16."""
+    B, Hq, H, d, W, T = 2, 2, 1, 64, 256, 4
+    g = torch.Generator().manual_seed(9)
+    dims = swa.Dims(B, Hq, H, d, W, 0.125, "f32")
+    cache, ref = swa.new_cache_q8(dims, fmt, DEV), q8.RollingCacheQ8(B, H, W, d, fmt)
+    for s in range(0, pos, W):
+        n = min(W, pos - s)
+        k, v = bf16(torch.randn(B, n, H, d, generator=g)), sized(g, [2.0 ** -20], B, n, H, d, W)
+        swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([s] * B), i32([n] * B))
+        q8.append(ref, k, v, [s] * B, [n] * B)
+    q, k, v = bf16(torch.randn(B, T, Hq, d, generator=g)), bf16(torch.randn(B, T, H, d, generator=g)), sized(g, [2.0 ** -20], B, T, H, d, W)
+    k[0, 2:] *= 2.0 ** 40              # sequence 0: keys; its last rows attend to one row alone
+    v[1, 2:] *= 2.0 ** 40
+    o = torch.full((B, T, Hq, d), float("nan"), device=DEV)
+    swa.prefill_chunk_q8(dims, o, q.to(DEV), k.to(DEV), v.to(DEV), cache, i32([pos] * B), i32([T] * B),
+                         swa.prefill_workspace_q8(dims, T, DEV))
+    want, spread = q8.prefill_chunk(ref, q, k, v, [pos] * B, [T] * B, dims.scale)
+    close(o[:, :2], want[:, :2], spread[:, :2], "rows before the large ones")
+    close(o[1, 2:], want[1, 2:], spread[1, 2:], "rows of large values")
+    swa.device_status()
+
+
+def test_a_chunk_over_a_tail_of_far_sizes():
+    """A row of the block being filled that has next to no weight, and values 2^45 times the others'."""
+    B, Hq, H, d, W, pos, T = 1, 4, 1, 64, 256, 13, 2
+    g = torch.Generator().manual_seed(10)
+    dims = swa.Dims(B, Hq, H, d, W, 0.125, "f32")
+    cache, ref = swa.new_cache_q8(dims, "e4m3", DEV), q8.RollingCacheQ8(B, H, W, d, "e4m3")
+    k, v = bf16(0.25 * torch.randn(B, pos, H, d, generator=g)), sized(g, [1.0], B, pos, H, d, W)
+    q = bf16(torch.rand(B, T, Hq, d, generator=g) + 0.5)
+    k[:, 7], v[:, 7] = -8.0, v[:, 7] * 2.0 ** 45       # a weight below 2^-46 for every query
+    swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([0]), i32([pos]))
+    q8.append(ref, k, v, [0], [pos])
+    kc, vc = bf16(0.25 * torch.randn(B, T, H, d, generator=g)), sized(g, [1.0], B, T, H, d, W)
+    o = torch.full((B, T, Hq, d), float("nan"), device=DEV)
+    swa.prefill_chunk_q8(dims, o, q.to(DEV), kc.to(DEV), vc.to(DEV), cache, i32([pos]), i32([T]),
+                         swa.prefill_workspace_q8(dims, T, DEV))
+    want, spread = q8.prefill_chunk(ref, q, kc, vc, [pos], [T], dims.scale)
+    close(o, want, spread, "chunk")
+    swa.device_status()
