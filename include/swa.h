@@ -247,7 +247,8 @@ SWA_API int swa_decode_static(const swa_dims* dims, void* out, const void* q, co
 typedef struct swa_q8_cache {
     void*   k;       /* [B][Hkv][W][d], one byte an element                         */
     void*   v;
-    float*  k_scale; /* [B][Hkv][ceil(W / 64)] powers of two                         */
+    float*  k_scale; /* [B][Hkv][ceil(W / 64)] powers of two; a block that was not   */
+                     /* written by these calls may have any normal scale > 0         */
     float*  v_scale;
     void*   k_tail;  /* [B][Hkv][64][d] bf16: row i is slot 64 j + i of the block j  */
     void*   v_tail;  /* that the sequence's next token falls into, if i is before it */

@@ -369,10 +369,12 @@ class CacheQ8:
     """One layer's rolling cache in 8 bits (mirrors ``swa_q8_cache``).
 
     ``k``, ``v`` [B, Hkv, W, d] float8_e4m3fn or int8; ``k_scale``, ``v_scale``
-    [B, Hkv, ceil(W / 64)] float32, powers of two: a row stands for its 8-bit
-    numbers times the scale of its block of 64 slots; ``k_tail``, ``v_tail``
-    [B, Hkv, 64, d] bf16: the rows so far of the block being filled.  The tensors
-    are used where they are; keep the handle and pass it to every call.
+    [B, Hkv, ceil(W / 64)] float32: a row stands for its 8-bit numbers times the
+    scale of its block of 64 slots (the calls write powers of two; blocks filled
+    from elsewhere may have any normal scale > 0, of which a chunk that is written
+    out in bf16 rounds the products); ``k_tail``, ``v_tail`` [B, Hkv, 64, d] bf16:
+    the rows so far of the block being filled.  The tensors are used where they
+    are; keep the handle and pass it to every call.
     """
 
     k: torch.Tensor

@@ -32,8 +32,6 @@ __device__ __forceinline__ int scale_exp(uint32_t amax) {
 
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// Exponent of a (positive, normal) power of two.
-__device__ __forceinline__ int exp_of(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

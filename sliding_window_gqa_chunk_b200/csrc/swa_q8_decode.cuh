@@ -14,8 +14,8 @@
 // the time that the bytes take, and its operands would have to be written back to
 // shared memory in 16 bits.
 //
-// Scales.  A block's key scale multiplies its scores.  Its value scale 2^v is put into
-// the exponent of the softmax: with x the score in log2 units, the weight of a slot is
+// Scales.  A block's key scale multiplies its scores.  Its value scale 2^v (v whole for scales that
+// the library writes) is put into the exponent of the softmax: with x the score in log2 units, the weight of a slot is
 // w = 2^(x + v - m + 15), where the running m is the maximum of x + v rather than of x.
 // The numbers of a block's values reach the top of their format, so w orders the
 // slots by what they can add to the output and is at most 2^15: f16 keeps 11 bits of the
@@ -278,6 +278,12 @@ struct State {
   float m[2], r[2], l[2];
   float o[Q8Frag<D>::kMTiles][4];
 };
+
+// log2 of a block's value scale, exact for the powers of two that the library writes itself.
+__device__ __forceinline__ float log2_of(float s) {
+  const uint32_t bits = __float_as_uint(s);
+  return (float)((int)(bits >> 23) - 127) + __log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+}
 
 // Factor of the scores from those of the head and of the keys, both > 0.  Kept
 // where a masked -inf stays -inf and a dot product of 0 stays 0.
@@ -738,7 +744,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
 
     tile = take();
     if (!ok) break;
-    float vsize = (float)q8::exp_of(vs);
+    float vsize = log2_of(vs);
     // a block of zeros, or one that needs no scale: its bytes tell
     if (vs == 1.f && all_zero<D, FMT>(tile, lo - x0, hi - x0)) vsize = kZeroExp;
     uint32_t pb[NT][kSubs][2];
