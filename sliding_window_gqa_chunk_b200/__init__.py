@@ -129,9 +129,11 @@ class Dims:
         return _CDims(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.window,
                       float(self.scale), _DTYPES[self.out_dtype])
 
-    @functools.cached_property
+    @property
     def _record(self) -> _CDims:
-        return self.c()
+        # made once, whichever threads ask first: a call may still read it while another one asks
+        record = self.__dict__.get("_record_kept")
+        return record if record is not None else self.__dict__.setdefault("_record_kept", self.c())
 
     @functools.cached_property
     def _dims_addr(self) -> int:
