@@ -139,8 +139,8 @@ class Dims:
     def _dims_addr(self) -> int:
         return ctypes.addressof(self._record)
 
-    def __reduce__(self):       # a copy makes its own record
-        return Dims, tuple(getattr(self, f.name) for f in dataclasses.fields(self))
+    def __getstate__(self):     # a copy makes its own record
+        return {k: v for k, v in self.__dict__.items() if k not in ("_record_kept", "_dims_addr")}
 
     @property
     def torch_out_dtype(self) -> torch.dtype:

@@ -1,5 +1,8 @@
 """The record of a Dims that the calls of the 8-bit cache read by its address."""
+import copy
 import ctypes
+import dataclasses
+import pickle
 import threading
 
 import sliding_window_gqa_chunk_b200 as swa
@@ -29,3 +32,17 @@ def test_threads_that_ask_first_together_get_one_record(monkeypatch):
         t.join()
     monkeypatch.undo()
     assert made == [ctypes.addressof(d._record)] * 2 == [d._dims_addr] * 2
+
+
+@dataclasses.dataclass(frozen=True)
+class Layer(swa.Dims):
+    name: str = "?"
+
+
+def test_copies_of_a_kind_of_dims_stay_of_their_kind():
+    a = Layer(1, 2, 1, 16, 64, 0.25, "bf16", "first")
+    object.__setattr__(a, "note", [1])
+    address = a._dims_addr
+    for b in (copy.copy(a), copy.deepcopy(a), pickle.loads(pickle.dumps(a))):
+        assert type(b) is Layer and b == a and b.note == [1]
+        assert b._dims_addr != address and b._record.batch == 1
