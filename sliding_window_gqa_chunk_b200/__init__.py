@@ -499,13 +499,17 @@ def new_rope(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, 
     * "linear": all positions divided by scale;
     * "base": base raised so that the slowest pair turns scale times slower and the fastest as before;
     * "yarn": pairs that turn more than 32 times over original_length are kept, those that turn less
-      than once are slowed by scale, linearly in the number of turns between, and turned elements are
-      multiplied by 0.1 ln(scale) + 1.
+      than once are slowed by scale, and turned elements are multiplied by 0.1 ln(scale) + 1.  Between,
+      the share that is slowed grows linearly with the pair's index, from the last index (rounded down)
+      with 32 turns to the first (rounded up) with one, as models with such tables are trained.  (The
+      method's paper writes the ramp in the number of turns: for that, pass Rope a table.)
     """
     if scaling not in ("none", "linear", "base", "yarn"):
         raise ValueError(f"scaling {scaling!r}: expected none, linear, base or yarn")
     if rotary_dim < 2 or rotary_dim % 2 or not base > 0 or not scale > 0 or not original_length > 0:
         raise ValueError("rotary_dim must be even and positive, base, scale and original_length positive")
+    if scaling == "yarn" and not base > 1:
+        raise ValueError("yarn needs a base above 1: the pairs' turns have to fall with their index")
     if scaling == "base" and rotary_dim > 2:
         base = base * scale ** (rotary_dim / (rotary_dim - 2))
     freq = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
@@ -513,9 +517,15 @@ def new_rope(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, 
     if scaling == "linear":
         freq = freq / scale
     elif scaling == "yarn":
+        def index(turns):       # of the pair that turns so often: original_length base ** (-2 i / rotary_dim) = 2 pi turns
+            return rotary_dim / 2 * math.log(original_length / (2 * math.pi * turns)) / math.log(base)
+
+        low, high = max(math.floor(index(32)), 0), min(math.ceil(index(1)), rotary_dim - 1)
+        slowed = ((torch.arange(rotary_dim // 2, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0, 1)
+        # where the ramp's ends fall outside the table
         turns = original_length * freq / (2 * math.pi)
-        keep = ((turns - 1) / 31).clamp(0, 1)
-        freq = freq * keep + freq / scale * (1 - keep)
+        slowed = torch.where(turns > 32, 0.0, torch.where(turns < 1, 1.0, slowed))
+        freq = freq * (1 - slowed) + freq / scale * slowed
         factor = 0.1 * math.log(scale) + 1 if scale > 1 else 1.0
     return Rope(freq.float().to(device), interleaved, factor)
 
