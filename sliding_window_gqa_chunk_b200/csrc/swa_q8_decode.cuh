@@ -923,23 +923,43 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
   }
 }
 
-// Merge of the per-split partials: grid B * Hq, a thread to four elements.
+// Merge of the per-split partials: grid B * Hq, a warp; lanes share the splits' (m, r, l), then each has four elements.
+// (One pair of 1024 blocks: 15.5 us, and 23.4 with every lane going through all splits' sums.)
 template <int D>
 __global__ void __launch_bounds__(32) swa_q8_decode_combine_kernel(const Q8DecodeParams p) {
+  __shared__ float weight[kSms];                     // a pair has at most a split for each SM
   wait_prior_grid();
   allow_next_grid();
   const size_t bh = blockIdx.x;
-  const int c = threadIdx.x;
-  if (c >= D / 4 || p.pos[bh / p.n_q_heads] < 0) return;
-  const int S = p.n_splits;
-  const float4* ml = reinterpret_cast<const float4*>(p.ws_ml) + bh * S;
-  const float4* o = reinterpret_cast<const float4*>(p.ws_o) + bh * S * (D / 4) + c;
+  if (p.pos[bh / p.n_q_heads] < 0) return;
+  const int S = p.n_splits, lane = threadIdx.x;
+  const float4* parts = reinterpret_cast<const float4*>(p.ws_ml) + bh * S;
   Four f;
+  for (int s = lane; s < S; s += 32) f.against(parts[s]);
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    f.m = fmaxf(f.m, __shfl_xor_sync(0xffffffffu, f.m, off));
+    f.r = fmaxf(f.r, __shfl_xor_sync(0xffffffffu, f.r, off));
+  }
+  for (int s = lane; s < S; s += 32) {
+    const float4 part = parts[s];
+    weight[s] = fast_exp2(part.x - f.m);
+    f.l += fast_exp2(part.y - f.r) * part.z;
+  }
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) f.l += __shfl_xor_sync(0xffffffffu, f.l, off);
+  __syncwarp();
+  if (lane >= D / 4) return;
+  const float4* o = reinterpret_cast<const float4*>(p.ws_o) + bh * S * (D / 4) + lane;
 #pragma unroll 8
-  for (int s = 0; s < S; ++s) f.against(ml[s]);
-#pragma unroll 8
-  for (int s = 0; s < S; ++s) f.add(ml[s], o[(size_t)s * (D / 4)]);
-  f.store(p.out, bh * (D / 4) + c, p.out_f32);
+  for (int s = 0; s < S; ++s) {
+    const float4 x = o[(size_t)s * (D / 4)];
+    f.o.x += weight[s] * x.x;
+    f.o.y += weight[s] * x.y;
+    f.o.z += weight[s] * x.z;
+    f.o.w += weight[s] * x.w;
+  }
+  f.store(p.out, bh * (D / 4) + lane, p.out_f32);
 }
 
 namespace {
