@@ -121,6 +121,10 @@ cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, int 
 // TMA box width (elements of d per box row) and swizzle span used by the prefill kernel.
 void prefill_map_geometry(int head_dim, int* box_elems, int* swizzle_bytes);
 
+// SMs of a B200, for the launch shapes of the 8-bit cache's steps and of the rotary positions.  A constant: the shape
+// of a decode step fixes the size of its workspace, which is a function of the dims and not of the current device.
+constexpr int kSms = 148;
+
 // The 8-bit rolling cache (swa_q8_cache of swa.h): blocks of kQ8Block slots.
 constexpr int kQ8Block = 64;
 

@@ -9,9 +9,9 @@
 // position s is the only one that reads the tail; its CTA also writes the new
 // tail, after that, so no CTA waits for another.
 //
-// Expand.  One 8-byte-per-element pass: 8-bit number times scale is exact in
-// bf16 (the scale is a power of two and no 8-bit number has more than 7
-// significant bits), rows of the block being filled are copied from the tail.
+// Expand.  One pass that reads a byte and writes two for each element: 8-bit
+// number times scale is exact in bf16 (the scales written here are powers of two
+// and no 8-bit number has more than 7 significant bits), rows of the block being filled are copied from the tail.
 // The slots that hold no position yet are written as zeros up to the end of
 // their 128-slot key tile, which the prefill kernel loads whole.
 #include "swa_common.cuh"

@@ -10,7 +10,6 @@ cudaError_t launch_q8_decode_128(const Q8DecodeParams& p, const Q8DecodeMaps& ma
 
 namespace {
 
-constexpr int kSms = 148;
 // Blocks of a window from which the pairs, where there are fewer than 148 / 8, go over all SMs and are
 // merged by a second kernel, not over clusters of 8: 8 pairs of 2048 blocks take 55 us and 74, of 512
 // blocks 23 either way, of 64 blocks 10.7 and 8.1.

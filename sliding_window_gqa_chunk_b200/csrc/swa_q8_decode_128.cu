@@ -15,7 +15,8 @@ int q8_clusters_at_once(int size) {
   if (size < 1 || size > kQ8MaxCluster || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int n = known[dev][size].load(std::memory_order_relaxed);
   if (n == 0) {
-    // any kernel that has an SM to itself: this one by its shared memory
+    // of the kernel that has an SM to itself by its shared memory; those of smaller heads, of which an SM holds two,
+    // are counted by the same number
     constexpr Q8Variant v = kQ8Variants[0];
     constexpr int smem = q8_smem_bytes<128, 1, v.warps, v.tiles>(true);
     auto kern = swa_q8_decode_kernel<128, 1, v.warps, v.tiles, v.per_sm, SWA_Q8_E4M3, false>;

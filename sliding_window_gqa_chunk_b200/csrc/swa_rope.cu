@@ -25,7 +25,6 @@ constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;      // tokens of a CTA
 constexpr int kHeads = 2;           // heads of a thread whose loads are in flight together
 constexpr int kCtasPerSm = 4;       // at 64 registers a thread
-constexpr int kSms = 148;
 constexpr int kMaxPairs = 64;       // rotary_dim <= 128
 
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
