@@ -363,6 +363,12 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
 
 }  // namespace
 
+// CTAs that an SM holds by their registers.  The CTA that has an SM to itself at d = 128 is not alone at d = 64 if it takes
+// 128 registers a thread and not 133: 512 pairs of 64 blocks 47.6 us for 56, 800 pairs 70 for 83 (74 pairs in clusters of
+// two 6.1 for 5.9).
+template <int D, int NT, int NW, bool CHUNK>
+constexpr int q8_ctas(int per) { return D == 64 && NT == 1 && NW == 8 && !CHUNK ? 2 : per; }
+
 // NT = number of 8-column n-tiles; NW = warps; R = tiles (a block's keys or
 // values) in a warp's ring; PER = CTAs an SM.
 //
@@ -372,7 +378,7 @@ __device__ __forceinline__ void softmax_step(State<D>& st, const float (&x)[SUB]
 // 1 .. t places after slot start mod W), and besides the tail's rows it sees the chunk's own up
 // to itself.  The cache stays as it is.
 template <int D, int NT, int NW, int R, int PER, int FMT, bool CHUNK>
-__global__ void __launch_bounds__(NW * 32, PER)
+__global__ void __launch_bounds__(NW * 32, q8_ctas<D, NT, NW, CHUNK>(PER))
 swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
   using F = Q8Frag<D>;
