@@ -239,6 +239,16 @@ SWA_API int swa_decode_static(const swa_dims* dims, void* out, const void* q, co
  * begun anew, if start_pos is 0).
  * Keys and values must be finite; what an infinity or a NaN leaves in its block
  * is not defined, and harms no other block, head or sequence.
+ *
+ * Precision.  Scores, softmax sums and outputs are in fp32.  A decode step and a
+ * chunk of few rows, which go straight over the bytes, hold a softmax weight to 11
+ * bits, or to 2^-40 of the largest product of a weight and its block's value scale;
+ * rows still in bf16 (the tail's, the new row, the chunk's) go through f16 with
+ * 2^-39 of the largest of the 16 that are taken together (a chunk takes rows of very
+ * different sizes one by one).  A longer chunk is written out in bf16 for the kernel
+ * of swa_prefill_chunk, which rounds the weights to bf16 (8 bits).  Which way a chunk
+ * goes is a function of dims and max_tokens: the same tokens cut into other chunks
+ * give outputs that differ by these roundings.
  */
 #define SWA_Q8_BLOCK 64
 #define SWA_Q8_E4M3 0 /* 8-bit floating point: 4 exponent bits, 3 mantissa bits, no infinities */
@@ -268,7 +278,8 @@ SWA_API int swa_q8_append(const swa_dims* dims, const swa_q8_cache* cache, const
 /*
  * swa_q8_prefill_workspace_size - bytes of device scratch swa_q8_prefill_chunk
  * needs: that of swa_prefill_chunk, and room for this layer's ring in bf16
- * (4 B Hkv W d bytes; one workspace serves all layers of a model in turn).
+ * (4 B Hkv W d bytes; one workspace serves all layers of a model in turn).  It is
+ * the same for every max_tokens, also for chunks of few rows, which do not use it.
  * Depends only on its arguments.  Returns 0 for invalid arguments.
  */
 SWA_API size_t swa_q8_prefill_workspace_size(const swa_dims* dims, int32_t max_tokens);

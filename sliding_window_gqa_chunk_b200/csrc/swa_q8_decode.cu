@@ -11,8 +11,8 @@ cudaError_t launch_q8_decode_128(const Q8DecodeParams& p, const Q8DecodeMaps& ma
 namespace {
 
 // Blocks of a window from which the pairs, where there are fewer than 148 / 8, go over all SMs and are
-// merged by a second kernel, not over clusters of 8: 8 pairs of 2048 blocks take 55 us and 74, of 512
-// blocks 23 either way, of 64 blocks 10.7 and 8.1.
+// merged by a second kernel, not over clusters of 8: 8 pairs of 2048 blocks take 54 us and 61, of 512
+// blocks 21 and 20, of 64 blocks 9.5 and 7.0.
 constexpr int kLongBlocks = 512;
 
 // Microseconds that `pairs` CTAs of variant v take in waves of what the SMs hold: a wave takes as long
@@ -35,8 +35,8 @@ double waves_us(int v, long long pairs, double blocks, int head_dim) {
 //    of at most 8 as long as each warp has one, or, for one token in a long window, over all SMs and
 //    merged by a second kernel.
 //  - More: a CTA to a pair, of the variant that waves_us() likes best.  Measured (us; variants 0, 1, 2):
-//    64 blocks, d = 128: 256 pairs 48, 48, 51; 320: 66, 80, 62; 512: 90, 87, 108; 768: 129, 128, 123;
-//    1184: 190, 200, 187.  4 blocks, 1024 pairs: 45, 28, 24.  63 blocks, d = 64, 800 pairs: 71, 86, 86.
+//    64 blocks, d = 128: 256 pairs 47, 47, 46; 320: 64, 75, 58; 512: 88, 84, 104; 768: 126, 123, 121;
+//    1184: 186, 192, 184.  4 blocks, 1024 pairs: 42, 27, 24.  63 blocks, d = 64, 800 pairs: 70, 70, 70.
 Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int head_dim, int groups, bool chunk, bool wide) {
   const long long units = (long long)batch * n_kv_heads * groups;
   const long long n_blocks = ((long long)window + kQ8Block - 1) / kQ8Block;
@@ -65,7 +65,7 @@ Q8DecodeSplit q8_decode_split(int batch, int n_kv_heads, int window, int head_di
 
 // Clusters do not cross the borders of the GPU's clusters of SMs, so of the larger sizes 148 SMs hold less than
 // 148 CTAs (105 in clusters of 7, 120 of 8): pairs that do not all fit at once would take twice as long.
-// 16 pairs of 64 blocks: 12.3 us in clusters of 8, 8.6 of 6; 48 pairs: 20.5 us of 3, 14.3 of 2.
+// 16 pairs of 64 blocks: 12.4 us in clusters of 8, 8.6 of 6; 48 pairs: 20.8 us of 3, 14.2 of 2.
 Q8DecodeSplit q8_fit_clusters(Q8DecodeSplit s, long long units, int window) {
   const long long n_blocks = ((long long)window + kQ8Block - 1) / kQ8Block;
   for (int size = s.n_splits - 1; s.cluster && size >= 1; --size) {
@@ -84,10 +84,10 @@ Q8DecodeSplit q8_fit_clusters(Q8DecodeSplit s, long long units, int window) {
 // however few of them there are.  Over the bytes go up to 128 columns; what the SMs hold at once (up to 512
 // rows, which one CTA of a pair reads alone); and up to 256 columns of up to 64 rows in two waves (of windows
 // of up to 8192: the written-out way has less to do before the first key and less for each).  Measured over the
-// bytes and written out (us, W = 4096, d = 128; 32 query heads over 8): 16 sequences x 4 rows 29, 205; 16 x 32
-// rows 217, 209; 1 x 64 rows 27, 49; 2 x 64 49, 55; 4 x 33 54, 73; 4 x 48 79, 74; 1 x 128 51, 50.  4 over 1:
-// 1 x 512 rows 37, 42; 1 x 1024 88, 43.  1 over 1: 1 x 512 24, 38; 1 x 1024 40, 38; 1 x 2048 70, 37.  In two
-// waves: 8 over 8, W = 7215, 3 x 164 rows 99, 83; 16 over 4, W = 16270, 3 x 53 184, 116.
+// bytes and written out (us, W = 4096, d = 128; 32 query heads over 8): 16 sequences x 4 rows 31, 208; 16 x 32
+// rows 192, 212; 1 x 64 rows 28, 50; 2 x 64 50, 55; 4 x 33 57, 74; 4 x 48 83, 75; 1 x 128 53, 51.  4 over 1:
+// 1 x 512 rows 39, 43; 1 x 1024 94, 43.  1 over 1: 1 x 512 26, 37; 1 x 1024 44, 38; 1 x 2048 75, 37.  In two
+// waves: 8 over 8, W = 7215, 3 x 164 rows 91, 83; 16 over 4, W = 16270, 3 x 53 161, 116.
 int q8_chunk_groups(long long rows, int group, long long pairs, int window) {
   const long long columns = rows * group, groups = columns > 8 ? (columns + 15) / 16 : 1, units = pairs * groups;
   const bool over_bytes = columns <= 128 || (units <= kSms && rows <= 512) ||

@@ -6,7 +6,7 @@
 // for all its heads: the CTA computes the cos and sin of its tokens once into
 // shared memory, and each thread keeps those of its 8 pairs in registers
 // while it goes through its share of the heads, two at a time: 4096 tokens of
-// 40 heads of 128 take 17.3 us (4.8 TB/s; 16384 tokens 56.7, 5.9 TB/s), one
+// 40 heads of 128 take 17.4 us (4.8 TB/s; 16384 tokens 56.5, 5.9 TB/s), one
 // head at a time with 5 CTAs an SM 18.1, three with 3 CTAs 17.9.  A thread's unit is 16
 // elements of a head, two 16-byte pieces that hold whole pairs: [8c, 8c + 8)
 // and [r/2 + 8c, ...) with halves, [16c, 16c + 16) interleaved; pair 8c + i is
@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) swa_rope_kernel(const Ro
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   // As many tokens to a CTA as leave the last wave of CTAs full, but not so many that a token has less than
   // four threads for each unit (below 16 heads, one for every eight), or than 16 (24 and 32: the same
-  // up to 10 % slower): 4096 tokens take one wave of 586 CTAs of 7; 12000 two of 8 and a short third, 42.8 us,
-  // and with CTAs of 11 45.6.
+  // up to 10 % slower): 4096 tokens of 40 heads of 128 take one wave of 586 CTAs of 7; 12000 three of CTAs of 7, the last
+  // one nearly full, 42.8 us (two and a half waves of CTAs of 8 42.5, two of CTAs of 11 45.6).
   const int units = p.head_dim / 16, heads = p.n_q_heads + p.n_kv_heads;
   const int share = heads < 16 ? (heads + 7) / 8 : 4, cap = kThreads / (units * share);
   const int most = cap < kMaxTokens ? cap : kMaxTokens;
