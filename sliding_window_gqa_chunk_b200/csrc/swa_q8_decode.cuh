@@ -14,22 +14,25 @@
 // the time that the bytes take, and its operands would have to be written back to
 // shared memory in 16 bits.
 //
-// Scales.  A block's key scale multiplies its scores.  Its value scale 2^v (v whole for scales that
-// the library writes) is put into the exponent of the softmax: with x the score in log2 units, the weight of a slot is
-// w = 2^(x + v - m + 15), where the running m is the maximum of x + v rather than of x.
-// The numbers of a block's values reach the top of their format, so w orders the
-// slots by what they can add to the output and is at most 2^15: f16 keeps 11 bits of the
-// weights down to 2^-29 of the largest.  The softmax sum is that of 2^(x - r), in fp32, against
-// a score r of its own: the first block's largest, 2^40 of which may pass before it moves.  It is
-// taken from the weights, w 2^(m - v - 15 - r), but where these have lost it (m above x + v by
-// more than 2^55: values of very different sizes), from the scores.  A block of zeros has a scale
-// of 1 that says nothing of its size: it is told from others of that scale by its bytes, and, as
-// zero rows in bf16, takes a scale below all others, which moves no m.  Q goes to f16 with one power
-// of two for each head (its largest magnitude to [2^14, 2^15)): its 8 bits are kept in all elements
-// above 2^-28 of the largest.  The rows of the block being filled (at most 64, in bf16) and a chunk's
-// own go through the same products, 16 rows with a power of two of their own at a time.  In a chunk
-// that may be a row that a query does not see: where sizes differ by 2^16 the rows go one by one.
-// (16 x 4 rows 31.1 us for it, 30.6 without; with powers of its own for each row 32.0.)
+// Scales. A block's key scale multiplies its scores. Its value scale 2^v (v whole for
+// scales that the library writes) is put into the exponent of the softmax: with x the
+// score in log2 units, the weight of a slot is w = 2^(x + v - m + 15), where the running m
+// is the maximum of x + v rather than of x. The numbers of a block's values reach the top
+// of their format, so w orders the slots by what they can add to the output and is at most
+// 2^15: f16 keeps 11 bits of the weights down to 2^-29 of the largest. The softmax sum is
+// that of 2^(x - r), in fp32, against a score r of its own: the first block's largest,
+// 2^40 of which may pass before it moves. (m, r and the exponents between them are whole
+// multiples of one step, so what rounds m and r cancels for scores up to 2^22.) It is
+// taken from the weights, w 2^(m - v - 15 - r), but where these have lost it (m above x +
+// v by more than 2^55: values of very different sizes), from the scores. A block of zeros
+// has a scale of 1 that says nothing of its size: it is told from others of that scale by
+// its bytes, and, as zero rows in bf16, takes a scale below all others, which moves no m.
+// Q goes to f16 with one power of two for each head (its largest magnitude to [2^14,
+// 2^15)): its 8 bits are kept in all elements above 2^-28 of the largest. The rows of the
+// block being filled (at most 64, in bf16) and a chunk's own go through the same products,
+// 16 rows with a power of two of their own at a time. In a chunk that may be a row that a
+// query does not see: where sizes differ by 2^16 the rows go one by one. (16 x 4 rows 31.1
+// us for it, 30.6 without; with powers of its own for each row 32.0.)
 //
 // Bytes.  The bound is HBM: 538 MB for 64 sequences of W = 4096 with 8 kv heads of 128
 // take 83 us (6.5 TB/s; a copy reaches 6.56).  Each warp streams its blocks through

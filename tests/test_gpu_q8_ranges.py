@@ -182,3 +182,27 @@ def test_a_chunk_over_a_tail_of_far_sizes():
     want, spread = q8.prefill_chunk(ref, q, kc, vc, [pos], [T], dims.scale)
     close(o, want, spread, "chunk")
     swa.device_status()
+
+
+@pytest.mark.parametrize("log2_score", [6, 12, 17, 22])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,Hq,H,d,W,pos", [(2, 4, 2, 128, 256, 700), (1, 12, 1, 128, 140 * 64, 9100), (150, 1, 1, 16, 320, 333), (1, 4, 1, 64, 1900 * 64, 4000)])
+def test_large_scores(B, Hq, H, d, W, pos, fmt, log2_score):
+    """Keys that are whole multiples of the query, with scores up to 2^22 (the documented limit) on 16 levels: equal scores
+    share the weight equally, and value scales that differ from block to block count in full beside maxima of this size."""
+    g = torch.Generator().manual_seed(log2_score)
+    u = torch.randint(0, 2, (d,), generator=g) * 2.0 - 1.0
+    # u . u = d: level c of 1 .. 16 gives a score of c / 16 2^log2_score
+    dims = swa.Dims(B, Hq, H, d, W, 2.0 ** log2_score / (16 * d), "f32")
+    cache, ref = swa.new_cache_q8(dims, fmt, DEV), q8.RollingCacheQ8(B, H, W, d, fmt)
+
+    def keys(n):
+        return bf16(torch.randint(1, 17, (B, n, H, 1), generator=g) * u)
+
+    for s in range(0, pos, 256):
+        n = min(256, pos - s)
+        k, v = keys(n), sized(g, [1.0, 2.0 ** -3, 2.0 ** 5], B, n, H, d, W, s)
+        swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([s] * B), i32([n] * B))
+        q8.append(ref, k, v, [s] * B, [n] * B)
+    q = bf16(u.expand(B, 3, Hq, d).contiguous())
+    run(dims, cache, ref, q, keys(3), sized(g, [1.0, 2.0 ** -3, 2.0 ** 5], B, 3, H, d, W, pos), [pos] * B, 3)
