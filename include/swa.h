@@ -240,17 +240,18 @@ SWA_API int swa_decode_static(const swa_dims* dims, void* out, const void* q, co
  * Keys and values must be finite; what an infinity or a NaN leaves in its block
  * is not defined, and harms no other block, head or sequence.
  *
- * Precision.  Scores, softmax sums and outputs are in fp32; scores (scale q . k)
- * must not exceed 2^22 in size (2^12 over blocks whose value scale is not a power of
- * two).  A decode step and a chunk of few rows, which go
- * straight over the bytes, hold a softmax weight to 11 bits, or to 2^-40 of the
- * largest product of a weight and its block's value scale; rows still in bf16 (the
- * tail's, the new row, the chunk's) go through f16 with 2^-39 of the largest of the
- * 16 that are taken together (a chunk takes rows of very different sizes one by
- * one).  A longer chunk is written out in bf16 for the kernel of swa_prefill_chunk,
- * which rounds the weights to bf16 (8 bits).  Which way a chunk goes is a function of
- * dims and max_tokens: the same tokens cut into other chunks give outputs that differ
- * by these roundings.
+ * Precision.  Scores, softmax sums and outputs are in fp32.  A decode step and a
+ * chunk of few rows, which go straight over the bytes, hold a softmax weight to 11
+ * bits, or to 2^-40 of the largest product of a weight and its block's value scale;
+ * rows still in bf16 (the tail's, the new row, the chunk's) go through f16 with
+ * 2^-39 of the largest of the 16 that are taken together (a chunk takes rows of very
+ * different sizes one by one).  Their scores (scale q . k) must not exceed 2^23 in
+ * size, or 2^12 over blocks whose value scale is not a power of two: where a row's
+ * largest is above 2^23.5 its output is not defined and SWA_ERR_DEVICE_ARG is raised
+ * in the device status word.  A longer chunk is written out in bf16 for the kernel of
+ * swa_prefill_chunk, which rounds the weights to bf16 (8 bits).  Which way a chunk
+ * goes is a function of dims and max_tokens: the same tokens cut into other chunks
+ * give outputs that differ by these roundings.
  */
 #define SWA_Q8_BLOCK 64
 #define SWA_Q8_E4M3 0 /* 8-bit floating point: 4 exponent bits, 3 mantissa bits, no infinities */

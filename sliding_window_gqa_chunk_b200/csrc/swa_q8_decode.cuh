@@ -22,8 +22,10 @@
 // 2^15: f16 keeps 11 bits of the weights down to 2^-29 of the largest. The softmax sum is
 // that of 2^(x - r), in fp32, against a score r of its own: the first block's largest,
 // 2^40 of which may pass before it moves. (m, r and the exponents between them are whole
-// multiples of one step, so what rounds m and r cancels for scores up to 2^22.) It is
-// taken from the weights, w 2^(m - v - 15 - r), but where these have lost it (m above x +
+// multiples of one step, so what rounds m and r cancels up to kMaxTop; larger ones are
+// refused: r and m - r kept apart, products as differences from r, gave the same
+// outputs for scores of any size, but one sequence 7.2 us and not 7.0, 16 x 4 rows 33.3 and
+// 31.5.) It is taken from the weights, w 2^(m - v - 15 - r), but where these have lost it (m above x +
 // v by more than 2^55: values of very different sizes), from the scores. A block of zeros
 // has a scale of 1 that says nothing of its size: it is told from others of that scale by
 // its bytes, and, as zero rows in bf16, takes a scale below all others, which moves no m.
@@ -196,6 +198,8 @@ __device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w, float s) {
 __device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
 // Whether magnitudes (bf16 bits) from `least` + 1 (none: ~0) to `most` lie further apart than one power of two serves all of them.
 __device__ __forceinline__ bool apart(uint32_t most, uint32_t least) { return (int)(most >> 7) - (int)(least >> 7) > 16; }
+// Largest score and value scale (log2) up to which every whole number counts beside it in fp32.
+constexpr float kMaxTop = 0x1p24f;
 // Exponent of the value scale of zeros: below that of all others by more than scores differ.
 constexpr float kZeroExp = -1000.f;
 
@@ -884,6 +888,7 @@ swa_q8_decode_kernel(const Q8DecodeParams p, const __grid_constant__ CUtensorMap
       ml[w] = sm_ml[w * G8 + h];
       f.against(ml[w]);
     }
+    if (c == 0 && h < live && fabsf(f.m) >= kMaxTop && f.m != -CUDART_INF_F) raise_status(p.status, SWA_ERR_DEVICE_ARG);
     if (f.m != -CUDART_INF_F) {
 #pragma unroll
       for (int w = 0; w < NW; ++w) f.add(ml[w], sm_o[(w * G8 + h) * D4 + (c ^ (h / 2 & 3))]);

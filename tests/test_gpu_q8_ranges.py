@@ -153,7 +153,7 @@ def test_rows_of_a_chunk_do_not_see_the_sizes_of_later_ones(pos, fmt):
         swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([s] * B), i32([n] * B))
         q8.append(ref, k, v, [s] * B, [n] * B)
     q, k, v = bf16(torch.randn(B, T, Hq, d, generator=g)), bf16(torch.randn(B, T, H, d, generator=g)), sized(g, [2.0 ** -20], B, T, H, d, W)
-    k[0, 2:] *= 2.0 ** 40              # sequence 0: keys; its last rows attend to one row alone
+    k[0, 2:] *= 2.0 ** 40              # sequence 0: keys
     v[1, 2:] *= 2.0 ** 40
     o = torch.full((B, T, Hq, d), float("nan"), device=DEV)
     swa.prefill_chunk_q8(dims, o, q.to(DEV), k.to(DEV), v.to(DEV), cache, i32([pos] * B), i32([T] * B),
@@ -161,7 +161,9 @@ def test_rows_of_a_chunk_do_not_see_the_sizes_of_later_ones(pos, fmt):
     want, spread = q8.prefill_chunk(ref, q, k, v, [pos] * B, [T] * B, dims.scale)
     close(o[:, :2], want[:, :2], spread[:, :2], "rows before the large ones")
     close(o[1, 2:], want[1, 2:], spread[1, 2:], "rows of large values")
-    swa.device_status()
+    with pytest.raises(swa.SwaError) as e:      # sequence 0's last rows have scores of 2^40
+        swa.device_status()
+    assert e.value.code == swa.SWA_ERR_DEVICE_ARG
 
 
 def test_a_chunk_over_a_tail_of_far_sizes():
@@ -184,12 +186,12 @@ def test_a_chunk_over_a_tail_of_far_sizes():
     swa.device_status()
 
 
-@pytest.mark.parametrize("log2_score", [6, 12, 17, 22])
+@pytest.mark.parametrize("log2_score", [6, 12, 17, 22, 23])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("B,Hq,H,d,W,pos", [(2, 4, 2, 128, 256, 700), (1, 12, 1, 128, 140 * 64, 9100), (150, 1, 1, 16, 320, 333), (1, 4, 1, 64, 1900 * 64, 4000)])
 def test_large_scores(B, Hq, H, d, W, pos, fmt, log2_score):
-    """Keys that are whole multiples of the query, with scores up to 2^22 (the documented limit) on 16 levels: equal scores
-    share the weight equally, and value scales that differ from block to block count in full beside maxima of this size."""
+    """Keys that are whole multiples of the query, with large scores on 16 levels: equal scores share the weight equally,
+    and value scales that differ from block to block count in full beside maxima of this size."""
     g = torch.Generator().manual_seed(log2_score)
     u = torch.randint(0, 2, (d,), generator=g) * 2.0 - 1.0
     # u . u = d: level c of 1 .. 16 gives a score of c / 16 2^log2_score
@@ -206,3 +208,30 @@ def test_large_scores(B, Hq, H, d, W, pos, fmt, log2_score):
         q8.append(ref, k, v, [s] * B, [n] * B)
     q = bf16(u.expand(B, 3, Hq, d).contiguous())
     run(dims, cache, ref, q, keys(3), sized(g, [1.0, 2.0 ** -3, 2.0 ** 5], B, 3, H, d, W, pos), [pos] * B, 3)
+
+
+@pytest.mark.parametrize("log2_score", [24, 40, 100])
+@pytest.mark.parametrize("chunk", [False, True])
+def test_scores_beyond_the_limit_are_reported(chunk, log2_score):
+    """One sequence of two has a row whose largest score, 2^log2_score or its negative, is past 2^23.5; the other is right."""
+    B, Hq, H, d, W, pos = 2, 4, 2, 64, 640, 300
+    g = torch.Generator().manual_seed(1)
+    for sign in (1.0, -1.0):
+        dims = swa.Dims(B, Hq, H, d, W, 2.0 ** log2_score / d, "f32")
+        cache, ref = swa.new_cache_q8(dims, "e4m3", DEV), q8.RollingCacheQ8(B, H, W, d, "e4m3")
+        k, v = torch.ones(B, pos, H, d, dtype=torch.bfloat16), sized(g, [1.0], B, pos, H, d, W)
+        swa.cache_append_q8(dims, cache, k.to(DEV), v.to(DEV), i32([0] * B), i32([pos] * B))
+        q8.append(ref, k, v, [0] * B, [pos] * B)
+        q = torch.full((B, 1, Hq, d), sign, dtype=torch.bfloat16)
+        q[1] = 0.0                          # scores of zero
+        o = torch.full((B, 1, Hq, d), float("nan"), device=DEV)
+        args = q.to(DEV), k[:, :1].contiguous().to(DEV), v[:, :1].contiguous().to(DEV)
+        if chunk:
+            swa.prefill_chunk_q8(dims, o, *args, cache, i32([pos] * B), i32([1] * B), swa.prefill_workspace_q8(dims, 1, DEV))
+        else:
+            swa.decode_q8(dims, o.view(B, Hq, d), *(x[:, 0] for x in args), cache, i32([pos] * B), swa.decode_workspace_q8(dims, DEV))
+        with pytest.raises(swa.SwaError) as e:
+            swa.device_status()
+        assert e.value.code == swa.SWA_ERR_DEVICE_ARG
+        want, spread = q8.prefill_chunk(ref, q, k[:, :1], v[:, :1], [pos] * B, [1] * B, dims.scale)
+        close(o[1:], want[1:], spread[1:], "the other sequence")
